@@ -8,32 +8,40 @@ current HIP stream.  All arithmetic runs in the library's HIP kernels; there is
 no fallback.  The functions carry the C names:
 
     lbq_layout, lbq_quantize, lbq_dequant, lbq_linear_fwd, lbq_linear_bwd_dx,
-    lbq_lora_fwd, lbq_nf4_codebook
+    lbq_lora_fwd, lbq_nf4_codebook, lbq_quantize_tokens, lbq_linear_fwd_tokens
+
+Beside them ``lbq_grad_norm``, ``lbq_clip_grad_norm_`` and ``LbqGradSet`` take a
+training step's gradient tensors as Python lists.
 
 Formats (cited by page title and section):
   * MinMax INT4 g128 / INT2 g64 -- GreenBit.AI, "只需单卡RTX 3090，低比特量化训练
     就能实现LLaMA-3 8B全参微调", section 模型量化;
   * NF4 with optional double quantization of the absmax -- "QLoRA技术在量化微调中的应用",
-    section QLoRA技术原理; bitsandbytes FSDP-QLoRA guide, step 2 parameter table.
+    section QLoRA技术原理; bitsandbytes FSDP-QLoRA guide, step 2 parameter table;
+  * INT8, symmetric, one scale per output channel; its forward multiplies tokens
+    quantized to 8 bits with one scale each.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 from typing import Optional
 
 import torch
 
-from ._lib import (LBQ_MAX_GROUP, LBQ_META_COMPACT, LBQ_META_F32, LBQ_MINMAX, LBQ_NF4, Desc, LbqError, QTensor, Sizes, check, lib,  # noqa: F401
+from ._lib import (LBQ_BF16, LBQ_F16, LBQ_F32, LBQ_INT8, LBQ_MAX_GROUP, LBQ_META_COMPACT, LBQ_META_F32,  # noqa: F401
+                   LBQ_MINMAX, LBQ_NF4, LBQ_NORM_2, LBQ_NORM_INF, Desc, Grad, LbqError, QTensor, Sizes, check, lib,
                    STATUS_CODE, EXPORTED, LIB_PATH)
 
 __all__ = [
     "QuantizedWeight", "make_desc", "lbq_layout", "lbq_quantize", "lbq_dequant",
     "lbq_linear_fwd", "lbq_linear_bwd_dx", "lbq_linear_bwd_dx_grouped", "lbq_lora_fwd", "lbq_nf4_codebook",
     "lbq_linear_workspace_bytes", "lbq_lora_workspace_bytes", "LbqError", "version",
+    "lbq_quantize_tokens", "lbq_linear_fwd_tokens", "lbq_grad_norm", "lbq_clip_grad_norm_", "LbqGradSet",
 ]
 
-_FMT = {"minmax": LBQ_MINMAX, "nf4": LBQ_NF4}
+_FMT = {"minmax": LBQ_MINMAX, "nf4": LBQ_NF4, "int8": LBQ_INT8}
 
 
 def version() -> str:
@@ -45,7 +53,8 @@ def make_desc(fmt: str, n: int, k: int, bits: int = 4, group: Optional[int] = No
     """Descriptor for W[n][k]. MinMax: bits 4/2, group 128/64 (default 128 for
     4-bit, 64 for 2-bit), ``compact`` for fp16 scales and packed zero points.
     NF4: absmax block 64, optional double quant (256), ``dq_offset`` for
-    double quantization with a per-tensor offset."""
+    double quantization with a per-tensor offset.  INT8: one scale per row
+    (``bits``, ``group`` and the other settings are not looked at)."""
     if fmt not in _FMT:
         raise ValueError(f"format must be one of {sorted(_FMT)}")
     d = Desc()
@@ -57,6 +66,9 @@ def make_desc(fmt: str, n: int, k: int, bits: int = 4, group: Optional[int] = No
         d.double_quant = 0
         d.dq_block = 0
         d.meta = LBQ_META_COMPACT if compact else LBQ_META_F32
+    elif fmt == "int8":
+        d.bits = 8
+        d.group = d.double_quant = d.dq_block = 0
     else:
         d.bits = 4
         d.group = 64 if group is None else group
@@ -85,6 +97,13 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device: torch.device):
+    """Context in which ``device`` is current: a launch needs its stream's device to be."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
@@ -122,7 +141,22 @@ class QuantizedWeight:
     def device(self) -> torch.device:
         return self.packed.device
 
+    def _check_int8(self) -> None:
+        n, k = self.desc.n, self.desc.k
+        if self.packed.numel() * self.packed.element_size() != n * k or not self.packed.is_contiguous():
+            raise ValueError(f"packed must hold the {n} x {k} codes, contiguous")
+        s = self.scales
+        if s is None or s.numel() != n or s.dtype != torch.float32 or not s.is_contiguous():
+            raise ValueError(f"scales must be {n} contiguous float32 values")
+        if s.device != self.packed.device or (self.out_rows is not None and self.out_rows.device != s.device):
+            raise ValueError("the tensors of a weight must be on one device")
+        o = self.out_rows
+        if o is not None and (o.numel() != n or o.dtype != torch.int32 or not o.is_contiguous()):
+            raise ValueError(f"out_rows must be {n} contiguous int32 values")
+
     def qtensor(self) -> QTensor:
+        if self.desc.format == LBQ_INT8:
+            self._check_int8()
         q = QTensor()
         q.packed = _ptr(self.packed)
         q.scales = _ptr(self.scales)
@@ -169,7 +203,9 @@ class QuantizedWeight:
         dev = torch.device(device)
         n, k = desc.n, desc.k
         qw = QuantizedWeight(desc, torch.empty((n, sz["packed"] // n), dtype=torch.uint8, device=dev))
-        if sz["scales"]:
+        if desc.format == LBQ_INT8:
+            qw.scales = torch.empty((n, 1), dtype=torch.float32, device=dev)
+        elif sz["scales"]:
             if desc.meta == LBQ_META_COMPACT:
                 qw.scales = torch.empty((n, sz["scales"] // 2 // n), dtype=torch.float16, device=dev)
             else:
@@ -192,9 +228,12 @@ def lbq_quantize(W: torch.Tensor, fmt: str = "minmax", bits: int = 4, group: Opt
     _need(W, "W", torch.float32)
     desc = make_desc(fmt, W.shape[0], W.shape[1], bits, group, double_quant, compact, dq_offset)
     qw = out if out is not None else QuantizedWeight.empty(desc, W.device)
+    if fmt == "int8" and (qw.desc.format, qw.n, qw.k, qw.device) != (LBQ_INT8, desc.n, desc.k, W.device):
+        raise ValueError("out must be an INT8 weight of W's shape on W's device")
     q = qw.qtensor()
-    check(lib.lbq_quantize(ctypes.byref(desc), W.data_ptr(), ctypes.byref(q), _stream(W.device)),
-          "lbq_quantize")
+    with _on(W.device):
+        check(lib.lbq_quantize(ctypes.byref(desc), W.data_ptr(), ctypes.byref(q), _stream(W.device)),
+              "lbq_quantize")
     qw.desc = desc
     return qw
 
@@ -205,8 +244,10 @@ def lbq_dequant(qw: QuantizedWeight, out: Optional[torch.Tensor] = None) -> torc
         out = torch.empty((qw.n, qw.k), dtype=torch.bfloat16, device=qw.device)
     _need(out, "out", torch.bfloat16, (qw.n, qw.k))
     q = qw.qtensor()
-    check(lib.lbq_dequant(ctypes.byref(qw.desc), ctypes.byref(q), out.data_ptr(), _stream(qw.device)),
-          "lbq_dequant")
+    _same_device(qw.device, out)
+    with _on(qw.device):
+        check(lib.lbq_dequant(ctypes.byref(qw.desc), ctypes.byref(q), out.data_ptr(), _stream(qw.device)),
+              "lbq_dequant")
     return out
 
 
@@ -216,6 +257,12 @@ def lbq_linear_workspace_bytes(qw: QuantizedWeight, m: int) -> int:
 
 def lbq_lora_workspace_bytes(qw: QuantizedWeight, m: int, r: int) -> int:
     return lib.lbq_lora_workspace_bytes(ctypes.byref(qw.desc), m, r)
+
+
+def _same_device(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"every tensor must be on {device}, got one on {t.device}")
 
 
 def _ws(nbytes: int, device) -> Optional[torch.Tensor]:
@@ -242,9 +289,11 @@ def lbq_linear_fwd(X: torch.Tensor, qw: QuantizedWeight, out: Optional[torch.Ten
     if workspace is None:
         workspace = _ws(nbytes, X.device)
     q = qw.qtensor()
-    check(lib.lbq_linear_fwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, out.data_ptr(),
-                             out.stride(0), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                             _stream(X.device)), "lbq_linear_fwd")
+    _same_device(X.device, qw.packed, out, workspace)
+    with _on(X.device):
+        check(lib.lbq_linear_fwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, out.data_ptr(),
+                                 out.stride(0), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                 _stream(X.device)), "lbq_linear_fwd")
     return out
 
 
@@ -262,8 +311,10 @@ def lbq_linear_fwd_noalloc(X: torch.Tensor, qw: QuantizedWeight, out: Optional[t
     if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
         raise ValueError("out must be bf16 [m, >=n] with unit column stride")
     q = qw.qtensor()
-    check(lib.lbq_linear_fwd_noalloc(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, out.data_ptr(),
-                                     out.stride(0), _stream(X.device)), "lbq_linear_fwd_noalloc")
+    _same_device(X.device, qw.packed, out)
+    with _on(X.device):
+        check(lib.lbq_linear_fwd_noalloc(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, out.data_ptr(),
+                                         out.stride(0), _stream(X.device)), "lbq_linear_fwd_noalloc")
     return out
 
 
@@ -303,9 +354,11 @@ def lbq_linear_fwd_grouped(X: torch.Tensor, qws, outs=None, workspace: Optional[
     nbytes = lib.lbq_linear_fwd_grouped_workspace_bytes(count, descs, m)
     if workspace is None:
         workspace = _ws(nbytes, X.device)
-    check(lib.lbq_linear_fwd_grouped(count, descs, qts, X.data_ptr(), m, ys, ldys, _ptr(workspace),
-                                     0 if workspace is None else workspace.numel(), _stream(X.device)),
-          "lbq_linear_fwd_grouped")
+    _same_device(X.device, workspace, *[q.packed for q in qws], *outs)
+    with _on(X.device):
+        check(lib.lbq_linear_fwd_grouped(count, descs, qts, X.data_ptr(), m, ys, ldys, _ptr(workspace),
+                                         0 if workspace is None else workspace.numel(), _stream(X.device)),
+              "lbq_linear_fwd_grouped")
     return outs
 
 
@@ -320,8 +373,10 @@ def lbq_linear_bwd_dx(dY: torch.Tensor, qw: QuantizedWeight,
         out = torch.empty((m, qw.k), dtype=torch.bfloat16, device=dY.device)
     _need(out, "out", torch.bfloat16, (m, qw.k))
     q = qw.qtensor()
-    check(lib.lbq_linear_bwd_dx(ctypes.byref(qw.desc), ctypes.byref(q), dY.data_ptr(), m,
-                                out.data_ptr(), _stream(dY.device)), "lbq_linear_bwd_dx")
+    _same_device(dY.device, qw.packed, out)
+    with _on(dY.device):
+        check(lib.lbq_linear_bwd_dx(ctypes.byref(qw.desc), ctypes.byref(q), dY.data_ptr(), m,
+                                    out.data_ptr(), _stream(dY.device)), "lbq_linear_bwd_dx")
     return out
 
 
@@ -345,8 +400,10 @@ def lbq_linear_bwd_dx_grouped(dYs, qws, out: Optional[torch.Tensor] = None) -> t
     descs = (Desc * count)(*[q.desc for q in qws])
     qts = (QTensor * count)(*[q.qtensor() for q in qws])
     dps = (ctypes.c_void_p * count)(*[d.data_ptr() for d in dYs])
-    check(lib.lbq_linear_bwd_dx_grouped(count, descs, qts, dps, m, out.data_ptr(), _stream(dYs[0].device)),
-          "lbq_linear_bwd_dx_grouped")
+    _same_device(dYs[0].device, out, *dYs, *[q.packed for q in qws])
+    with _on(dYs[0].device):
+        check(lib.lbq_linear_bwd_dx_grouped(count, descs, qts, dps, m, out.data_ptr(), _stream(dYs[0].device)),
+              "lbq_linear_bwd_dx_grouped")
     return out
 
 
@@ -369,10 +426,12 @@ def lbq_lora_fwd(X: torch.Tensor, qw: QuantizedWeight, A: torch.Tensor, B: torch
     if workspace is None:
         workspace = _ws(nbytes, X.device)
     q = qw.qtensor()
-    check(lib.lbq_lora_fwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, A.data_ptr(),
-                           B.data_ptr(), r, float(sigma), out.data_ptr(), out.stride(0),
-                           _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                           _stream(X.device)), "lbq_lora_fwd")
+    _same_device(X.device, qw.packed, A, B, out, workspace)
+    with _on(X.device):
+        check(lib.lbq_lora_fwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), m, A.data_ptr(),
+                               B.data_ptr(), r, float(sigma), out.data_ptr(), out.stride(0),
+                               _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream(X.device)), "lbq_lora_fwd")
     return out
 
 
@@ -409,10 +468,12 @@ def lbq_lora_bwd(X: torch.Tensor, dY: torch.Tensor, qw: QuantizedWeight, A: torc
     if workspace is None:
         workspace = _ws(nbytes, dev)
     q = qw.qtensor()
-    check(lib.lbq_lora_bwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), dY.data_ptr(), m,
-                           A.data_ptr(), B.data_ptr(), r, float(sigma), dX.data_ptr(), dA.data_ptr(),
-                           dB.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                           _stream(dev)), "lbq_lora_bwd")
+    _same_device(dev, qw.packed, dY, A, B, dX, dA, dB, workspace)
+    with _on(dev):
+        check(lib.lbq_lora_bwd(ctypes.byref(qw.desc), ctypes.byref(q), X.data_ptr(), dY.data_ptr(), m,
+                               A.data_ptr(), B.data_ptr(), r, float(sigma), dX.data_ptr(), dA.data_ptr(),
+                               dB.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream(dev)), "lbq_lora_bwd")
     return dX, dA, dB
 
 
@@ -462,3 +523,138 @@ class LbqLoraLinear(torch.nn.Module):
 
     def forward(self, X: torch.Tensor) -> torch.Tensor:
         return _LoraLinearFn.apply(X, self.A, self.B, self.qw, self.sigma)
+
+
+def lbq_quantize_tokens(X: torch.Tensor, out=None):
+    """(codes int8 [m, k], scales fp32 [m]) of the rows of bf16 X [m, k], one
+    scale a row (see ``lbq_quantize_tokens`` in lbq.h).  X may have any row
+    stride that is a multiple of 8; ``out`` takes a pair of such tensors."""
+    if not X.is_cuda or X.dtype != torch.bfloat16 or X.dim() != 2:
+        raise ValueError("X must be a bf16 device tensor [m, k]")
+    m, k = X.shape
+    if k > 1 and X.stride(1) != 1:
+        raise ValueError("X must have unit column stride")
+    codes, scales = out if out is not None else (torch.empty((m, k), dtype=torch.int8, device=X.device),
+                                                 torch.empty(m, dtype=torch.float32, device=X.device))
+    _need(codes, "codes", torch.int8, (m, k))
+    _need(scales, "scales", torch.float32, (m,))
+    _same_device(X.device, codes, scales)
+    ldx = X.stride(0) if m > 1 else k
+    with _on(X.device):
+        check(lib.lbq_quantize_tokens(X.data_ptr(), m, k, ldx, codes.data_ptr(), scales.data_ptr(), _stream(X.device)),
+              "lbq_quantize_tokens")
+    return codes, scales
+
+
+def lbq_linear_fwd_tokens(codes: torch.Tensor, scales: torch.Tensor, qw: QuantizedWeight,
+                          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = deq(codes) . deq(W)^T in bf16 for an INT8 weight and the tokens of
+    ``lbq_quantize_tokens`` (see ``lbq_linear_fwd_tokens`` in lbq.h).  ``out``
+    and ``qw.out_rows`` as in ``lbq_linear_fwd``."""
+    if codes.dim() != 2 or codes.shape[1] != qw.k:
+        raise ValueError(f"codes must be [m, {qw.k}]")
+    m, dev = codes.shape[0], codes.device
+    _need(codes, "codes", torch.int8)
+    _need(scales, "scales", torch.float32, (m,))
+    if out is None:
+        if qw.out_rows is not None:
+            raise ValueError("out must be given when out_rows is set")
+        out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=dev)
+    if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
+        raise ValueError("out must be bf16 [m, >=n] with unit column stride")
+    if qw.out_rows is None and out.shape[1] < qw.n:
+        raise ValueError(f"out must have at least {qw.n} columns")
+    _same_device(dev, scales, out, qw.packed, workspace)
+    if workspace is None:
+        workspace = _ws(lib.lbq_linear_fwd_tokens_workspace_bytes(ctypes.byref(qw.desc), m), dev)
+    q = qw.qtensor()
+    with _on(dev):
+        check(lib.lbq_linear_fwd_tokens(ctypes.byref(qw.desc), ctypes.byref(q), codes.data_ptr(), scales.data_ptr(), m,
+                                        out.data_ptr(), out.stride(0), _ptr(workspace),
+                                        0 if workspace is None else workspace.numel(), _stream(dev)),
+              "lbq_linear_fwd_tokens")
+    return out
+
+
+_GRAD_DTYPE = {torch.float32: LBQ_F32, torch.bfloat16: LBQ_BF16, torch.float16: LBQ_F16}
+_NORM_TYPE = {2.0: LBQ_NORM_2, float("inf"): LBQ_NORM_INF}
+
+
+class LbqGradSet:
+    """The gradient tensors of one training step, for their norm and clipping
+    (see ``lbq_grad_norm`` and ``lbq_clip_grads`` in lbq.h).  A program whose
+    gradient buffers live as long as the training run builds it once; a tensor
+    whose storage moved is looked up again at the next call.
+
+    ``grads``: contiguous fp32, bf16 or fp16 tensors on one device.  ``outs``:
+    where ``clip`` writes the scaled gradients (tensors of the same types and
+    sizes); by default it scales in place."""
+
+    def __init__(self, grads, outs=None):
+        self._grads = list(grads)
+        self._outs = self._grads if outs is None else list(outs)
+        if not self._grads:
+            raise ValueError("at least one gradient")
+        if len(self._outs) != len(self._grads):
+            raise ValueError("one output per gradient")
+        self.device = self._grads[0].device
+        if self.device.type != "cuda":
+            raise ValueError("gradients must be device tensors")
+        self._table = (Grad * len(self._grads))()
+        self._seen = None
+        self._look()
+
+    def _look(self) -> None:
+        """Fill the table from the tensors, unless all are where they were."""
+        seen = [t.data_ptr() for t in self._grads]
+        seen += [t.numel() for t in self._grads]
+        if self._outs is not self._grads:
+            seen += [t.data_ptr() for t in self._outs]
+            seen += [t.numel() for t in self._outs]
+        if seen == self._seen:
+            return
+        for i, (g, o) in enumerate(zip(self._grads, self._outs)):
+            if g.dtype not in _GRAD_DTYPE or not g.is_contiguous() or g.device != self.device:
+                raise ValueError(f"grads[{i}] must be a contiguous fp32, bf16 or fp16 tensor on {self.device}")
+            if o is not g and (o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous() or o.device != self.device):
+                raise ValueError(f"outs[{i}] must be a contiguous tensor of grads[{i}]'s type and size on {self.device}")
+            e = self._table[i]
+            e.grad, e.out, e.numel, e.dtype, e.reserved = g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype], 0
+        self._nbytes = lib.lbq_grad_workspace_bytes(len(self._grads), self._table)
+        self._seen = seen
+
+    def _call(self, norm_type: float, max_norm: Optional[float]) -> torch.Tensor:
+        if float(norm_type) not in _NORM_TYPE:
+            raise ValueError("norm_type must be 2 or inf")
+        kind = _NORM_TYPE[float(norm_type)]
+        self._look()
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        workspace = _ws(self._nbytes, self.device)
+        with _on(self.device):
+            if max_norm is None:
+                check(lib.lbq_grad_norm(len(self._grads), self._table, kind, norm.data_ptr(), _ptr(workspace), self._nbytes,
+                                        _stream(self.device)), "lbq_grad_norm")
+            else:
+                check(lib.lbq_clip_grads(len(self._grads), self._table, kind, float(max_norm), norm.data_ptr(),
+                                         _ptr(workspace), self._nbytes, _stream(self.device)), "lbq_clip_grads")
+        return norm
+
+    def norm(self, norm_type: float = 2.0) -> torch.Tensor:
+        """The norm over all the gradients, an fp32 device scalar."""
+        return self._call(norm_type, None)
+
+    def clip(self, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
+        """Scale the gradients so that their norm is at most ``max_norm``;
+        returns the norm before that, an fp32 device scalar."""
+        return self._call(norm_type, max_norm)
+
+
+def lbq_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
+    """Norm over all the values of ``grads`` (a list of tensors)."""
+    return LbqGradSet(grads).norm(norm_type)
+
+
+def lbq_clip_grad_norm_(grads, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
+    """Scale ``grads`` in place so that their norm over all the values is at
+    most ``max_norm``; returns the norm before that."""
+    return LbqGradSet(grads).clip(max_norm, norm_type)

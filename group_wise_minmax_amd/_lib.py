@@ -13,9 +13,12 @@ LIB_PATH = os.path.join(HERE, "liblbq.so")
 
 LBQ_MINMAX = 0
 LBQ_NF4 = 1
+LBQ_INT8 = 2
 LBQ_META_F32 = 0
 LBQ_META_COMPACT = 1
 LBQ_MAX_GROUP = 8
+LBQ_F32, LBQ_BF16, LBQ_F16 = 0, 1, 2
+LBQ_NORM_2, LBQ_NORM_INF = 0, 1
 
 STATUS = {
     0: "LBQ_OK", 1: "LBQ_E_NULL", 2: "LBQ_E_SHAPE", 3: "LBQ_E_FORMAT", 4: "LBQ_E_ALIGN",
@@ -28,6 +31,8 @@ EXPORTED = (
     "lbq_linear_fwd", "lbq_linear_fwd_noalloc", "lbq_linear_fwd_grouped_workspace_bytes", "lbq_linear_fwd_grouped",
     "lbq_linear_bwd_dx", "lbq_linear_bwd_dx_grouped", "lbq_lora_workspace_bytes", "lbq_lora_fwd",
     "lbq_lora_bwd_workspace_bytes", "lbq_lora_bwd",
+    "lbq_quantize_tokens", "lbq_linear_fwd_tokens_workspace_bytes", "lbq_linear_fwd_tokens",
+    "lbq_grad_workspace_bytes", "lbq_grad_norm", "lbq_clip_grads",
     "lbq_serialized_bytes", "lbq_serialize", "lbq_blob_desc", "lbq_deserialize",
     "lbq_nf4_codebook", "lbq_strerror", "lbq_last_error_detail", "lbq_version",
 )
@@ -51,6 +56,11 @@ class Sizes(ctypes.Structure):
                 ("absmax_scale", ctypes.c_size_t)]
 
 
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class LbqError(RuntimeError):
     def __init__(self, status: int, func: str, detail: str):
         self.status = status
@@ -65,7 +75,7 @@ def _load() -> ctypes.CDLL:
             "(there is no fallback implementation)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    DP, QP = ctypes.POINTER(Desc), ctypes.POINTER(QTensor)
+    DP, QP, GP = ctypes.POINTER(Desc), ctypes.POINTER(QTensor), ctypes.POINTER(Grad)
     sig = {
         "lbq_layout": (I32, [DP, ctypes.POINTER(Sizes)]),
         "lbq_quantize": (I32, [DP, P, QP, P]),
@@ -81,6 +91,12 @@ def _load() -> ctypes.CDLL:
         "lbq_lora_fwd": (I32, [DP, QP, P, I64, P, P, I32, ctypes.c_float, P, I64, P, SZ, P]),
         "lbq_lora_bwd_workspace_bytes": (SZ, [DP, I64, I32]),
         "lbq_lora_bwd": (I32, [DP, QP, P, P, I64, P, P, I32, ctypes.c_float, P, P, P, P, SZ, P]),
+        "lbq_quantize_tokens": (I32, [P, I64, I64, I64, P, P, P]),
+        "lbq_linear_fwd_tokens_workspace_bytes": (SZ, [DP, I64]),
+        "lbq_linear_fwd_tokens": (I32, [DP, QP, P, P, I64, P, I64, P, SZ, P]),
+        "lbq_grad_workspace_bytes": (SZ, [I32, GP]),
+        "lbq_grad_norm": (I32, [I32, GP, I32, P, P, SZ, P]),
+        "lbq_clip_grads": (I32, [I32, GP, I32, ctypes.c_float, P, P, SZ, P]),
         "lbq_serialized_bytes": (SZ, [DP]),
         "lbq_serialize": (I32, [DP, QP, P, SZ, P]),
         "lbq_blob_desc": (I32, [P, SZ, DP]),

@@ -115,7 +115,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     if (i < set.count) nstage = set.stage_end[i];
   const int64_t N = (int64_t)nstage * BNR;
   const int64_t KB = K * T::bits / 8;
-  const int64_t gpr = K / T::group;
+  int64_t gpr = 1;  // metadata entries a row (8-bit rows: one scale)
+  if constexpr (T::fmt != FMT_INT8) gpr = K / T::group;
 
   if constexpr (T::fmt == FMT_NF4) {
 #pragma unroll
@@ -146,7 +147,10 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     b.w = make_rsrc(w.packed, b.n * KB);
     b.d = make_rsrc(set.dy[i], (int64_t)m * b.n * 2);
     b.off = 0.f;
-    if constexpr (T::fmt == FMT_MINMAX) {
+    if constexpr (T::fmt == FMT_INT8) {
+      b.s = make_rsrc(w.scales, nblk * 4);
+      b.z = b.s;
+    } else if constexpr (T::fmt == FMT_MINMAX) {
       b.s = make_rsrc(w.scales, scale_byte_index<KIND>(nblk));
       b.z = make_rsrc(w.zeros, zero_byte_index<KIND>(nblk));
     } else if constexpr (T::dq) {
@@ -184,7 +188,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   const int q = lane & 15, c = 4 * wave + lg;
   const int64_t kp = k0 + 32 * wave;
   const uint32_t w_voff = (uint32_t)((4 * q + lg) * KB + kp * T::bits / 8);
-  const uint32_t g_voff = (uint32_t)((4 * q + lg) * gpr + kp / T::group);
+  uint32_t g_voff = (uint32_t)((4 * q + lg) * gpr);
+  if constexpr (T::fmt != FMT_INT8) g_voff += (uint32_t)(kp / T::group);
   // dY chunks of this thread: chunk ci = tid + NT*i -> row ci >> 3, chunk ci & 7.
   const int64_t d_row = m0 + (tid >> 3), d_col = 8 * (tid & 7);
   char* const wt_base = reinterpret_cast<char*>(&Wt[0][0]);
@@ -198,7 +203,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     for (int b = 0; b < TM; ++b) acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   u32x4_t dr[DCH];
-  u32x4_t wraw;  // 32 codes of row 4q + lg (2-bit: dwords 0 and 1)
+  u32x4_t wraw;  // 32 codes of row 4q + lg (2-bit: dwords 0 and 1; 8-bit: the first 16)
+  u32x4_t wraw2;  // 8-bit: the last 16
   float md_s;
   int md_i;
   float md_off = 0.f;  // the loaded stage's weight's offset (the binding may move on before the store)
@@ -217,14 +223,19 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
       dr[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r_d, d_voff, so, 0));
     }
     const int so = (int)(nt * KB);
-    if constexpr (T::bits == 4) {
+    if constexpr (T::bits == 8) {
+      wraw = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r_w, w_voff, so, 0));
+      wraw2 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r_w, w_voff + 16, so, 0));
+    } else if constexpr (T::bits == 4) {
       wraw = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r_w, w_voff, so, 0));
     } else {
       const auto v = __builtin_amdgcn_raw_buffer_load_b64(r_w, w_voff, so, 0);
       wraw = u32x4_t{v[0], v[1], 0u, 0u};
     }
     const int go = (int)(nt * gpr);
-    if constexpr (T::fmt == FMT_MINMAX && T::compact) {
+    if constexpr (T::fmt == FMT_INT8) {
+      md_s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r_s, g_voff * 4, go * 4, 0));
+    } else if constexpr (T::fmt == FMT_MINMAX && T::compact) {
       // fp16 scale bits and the packed zero byte, as loaded (decoded in
       // store_stage: a use here would make the wave wait for the load)
       md_s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b16(r_s, g_voff * 2, go * 2, 0));
@@ -249,8 +260,12 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
       *reinterpret_cast<u32x4_t*>(ds + swz(ci >> 3, ci & 7)) = dr[i];
     }
     // wr[r]: chunk lg (8 codes) of row 4q + r
-    uint32_t wr[4];
-    if constexpr (T::bits == 4) {
+    uint32_t wr[4], wr2[4];  // (8-bit: a chunk is two dwords, transposed apart)
+    if constexpr (T::bits == 8) {
+      wr[0] = wraw[0], wr[1] = wraw[2], wr[2] = wraw2[0], wr[3] = wraw2[2];
+      wr2[0] = wraw[1], wr2[1] = wraw[3], wr2[2] = wraw2[1], wr2[3] = wraw2[3];
+      transpose_rows4(wr2[0], wr2[1], wr2[2], wr2[3]);
+    } else if constexpr (T::bits == 4) {
       wr[0] = wraw[0], wr[1] = wraw[1], wr[2] = wraw[2], wr[3] = wraw[3];
     } else {
       wr[0] = wraw[0] & 0xFFFFu, wr[1] = wraw[0] >> 16, wr[2] = wraw[1] & 0xFFFFu, wr[3] = wraw[1] >> 16;
@@ -258,7 +273,9 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     transpose_rows4(wr[0], wr[1], wr[2], wr[3]);
     // scale (MinMax: and z*s; NF4: the block absmax) of row 4q + r
     float sc[4], zc[4];
-    if constexpr (T::fmt == FMT_MINMAX) {
+    if constexpr (T::fmt == FMT_INT8) {
+      gather_rows4(md_s, sc);
+    } else if constexpr (T::fmt == FMT_MINMAX) {
       float s_ = md_s;
       int z_ = md_i;
       if constexpr (T::compact) {
@@ -276,7 +293,11 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     float v[4][8];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if constexpr (T::fmt == FMT_MINMAX) {
+      if constexpr (T::fmt == FMT_INT8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[r][j] = (float)(int)(int8_t)(uint8_t)((j < 4 ? wr[r] : wr2[r]) >> (8 * (j & 3))) * sc[r];
+      } else if constexpr (T::fmt == FMT_MINMAX) {
         const float s = sc[r], zs = zc[r];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[r][j] = fmaf((float)code_of<T::bits>(wr[r], j), s, -zs);
@@ -498,6 +519,7 @@ BwdSet make_bwd_set(const WView* ws, const uint16_t* const* dys, int count) {
 
 hipError_t launch_bwd_dx(WKind kind, const WView& w, const uint16_t* dY, int64_t m,
                          uint16_t* dX, const LoraDx& lora, const Nf4Table& tab, hipStream_t s) {
+  if (kind == WK_I8) return BwdLauncher<WK_I8>::run(make_bwd_set(&w, &dY, 1), m, dX, lora, tab, s);
   return dispatch_kind<BwdLauncher>(kind, make_bwd_set(&w, &dY, 1), m, dX, lora, tab, s);
 }
 
@@ -507,6 +529,7 @@ hipError_t launch_bwd_dx_set(WKind kind, const WView* ws, const uint16_t* const*
   for (int i = 1; i < count; ++i)
     if (ws[i].k != ws[0].k) return hipErrorInvalidValue;
   const LoraDx none{nullptr, nullptr, 0, 0};
+  if (kind == WK_I8) return BwdLauncher<WK_I8>::run(make_bwd_set(ws, dys, count), m, dX, none, tab, s);
   return dispatch_kind<BwdLauncher>(kind, make_bwd_set(ws, dys, count), m, dX, none, tab, s);
 }
 

@@ -1,0 +1,171 @@
+// Symmetric 8-bit quantization of rows, and the standalone dequantize of
+// 8-bit weights.
+//
+// A row (an output channel of a weight, or a token of an activation) has one
+// scale s = fl(max|x| / 127), 1 when that is 0, and codes
+// q = clamp(rne(fl(x / s)), -127, 127).  Every fp32 step is one IEEE operation
+// rounded to nearest-even (contraction is off for this file here and on its
+// compile line).  The magnitudes are compared as integers (the bits without
+// the sign order like the values, infinities and NaN above every finite one),
+// so a row that holds an infinity or a NaN is seen as such: it gets the scale
+// NaN and codes 0, and only that token's outputs are NaN.
+//
+// Bound by memory: a row is read once and kept in registers between the
+// search for its largest magnitude and the division, up to 8192 values
+// (fp32) or 16384 (bf16) a workgroup; a longer row is read again, from L2.
+#pragma clang fp contract(off)
+
+#include "lbq_device.h"
+
+namespace lbq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Eight consecutive values of a row as they are stored.
+template <typename T>
+struct Chunk8;
+template <>
+struct Chunk8<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4_t*>(p);
+    b = *(reinterpret_cast<const f32x4_t*>(p) + 1);
+  }
+  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
+template <>
+struct Chunk8<uint16_t> {
+  u32x4_t v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ float at(int i) const { return (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t max_magnitude(const Chunk8<T>& c, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(c.at(i)) & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
+template <typename T>
+__device__ __forceinline__ u32x2_t codes_of(const Chunk8<T>& c, float s, bool finite) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // the quotient can pass 127 when s is subnormal and was rounded down
+    float q = __builtin_rintf(c.at(i) / s);
+    q = fminf(fmaxf(q, -127.f), 127.f);
+    w[i >> 2] |= ((uint32_t)(int)q & 0xFFu) << (8 * (i & 3));
+  }
+  return finite ? u32x2_t{w[0], w[1]} : u32x2_t{0u, 0u};
+}
+
+// One workgroup a row.  NC: chunks of 8 values a thread keeps (k <= 2048 * NC).
+template <typename T, int NC, bool KEEP>
+__global__ __launch_bounds__(kThreads) void k_i8_quant_rows(const T* __restrict__ X, int64_t ldx, int64_t k,
+                                                           int8_t* __restrict__ Q, float* __restrict__ scales) {
+  __shared__ uint32_t red[kThreads / 64];
+  const int64_t row = blockIdx.x;
+  const T* x = X + row * ldx;
+  int8_t* q = Q + row * k;
+  const int tid = threadIdx.x;
+  const int chunks = (int)(k / 8);
+  Chunk8<T> c[NC];
+  uint32_t m = 0;
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (tid + i * kThreads < chunks) c[i].load(x + 8 * (tid + i * kThreads));
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (tid + i * kThreads < chunks) m = max_magnitude(c[i], m);
+  } else {
+    for (int i = tid; i < chunks; i += kThreads) {
+      c[0].load(x + 8 * i);
+      m = max_magnitude(c[0], m);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t t = __shfl_xor(m, o);
+    m = t > m ? t : m;
+  }
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) m = red[i] > m ? red[i] : m;
+  const bool finite = m < 0x7F800000u;
+  float s = __uint_as_float(m) / 127.f;
+  if (s == 0.f) s = 1.f;
+  if (!finite) s = __uint_as_float(0x7FC00000u);
+  if (tid == 0) scales[row] = s;
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (tid + i * kThreads < chunks)
+        *reinterpret_cast<u32x2_t*>(q + 8 * (tid + i * kThreads)) = codes_of(c[i], s, finite);
+  } else {
+    for (int i = tid; i < chunks; i += kThreads) {
+      c[0].load(x + 8 * i);
+      *reinterpret_cast<u32x2_t*>(q + 8 * i) = codes_of(c[0], s, finite);
+    }
+  }
+}
+
+template <typename T, int NC, bool KEEP>
+hipError_t launch_rows(const T* X, int64_t rows, int64_t k, int64_t ldx, int8_t* Q, float* scales, hipStream_t s) {
+  hipLaunchKernelGGL((k_i8_quant_rows<T, NC, KEEP>), dim3((unsigned)rows), dim3(kThreads), 0, s, X, ldx, k, Q, scales);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(kThreads) void k_i8_dequant(const int8_t* __restrict__ Q,
+                                                        const float* __restrict__ scales, int k,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t row = blockIdx.x;
+  const float s = scales[row];
+  const int8_t* q = Q + row * k;
+  uint16_t* o = out + row * k;
+  for (int i = 8 * threadIdx.x; i < k; i += 8 * kThreads) {
+    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(q + i);
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = v[j >> 1] >> (16 * (j & 1));
+      d[j] = cvt_pk_bf16((float)(int8_t)(uint8_t)w * s, (float)(int8_t)(uint8_t)(w >> 8) * s);
+    }
+    *reinterpret_cast<u32x4_t*>(o + i) = u32x4_t{d[0], d[1], d[2], d[3]};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_i8_quant_f32(const float* W, int64_t n, int64_t k, int8_t* Q, float* scales, hipStream_t s) {
+  if (k <= 2048) return launch_rows<float, 1, true>(W, n, k, k, Q, scales, s);
+  if (k <= 4096) return launch_rows<float, 2, true>(W, n, k, k, Q, scales, s);
+  if (k <= 8192) return launch_rows<float, 4, true>(W, n, k, k, Q, scales, s);
+  return launch_rows<float, 1, false>(W, n, k, k, Q, scales, s);
+}
+
+hipError_t launch_i8_quant_bf16(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Q, float* scales,
+                                hipStream_t s) {
+  if (k <= 2048) return launch_rows<uint16_t, 1, true>(X, m, k, ldx, Q, scales, s);
+  if (k <= 4096) return launch_rows<uint16_t, 2, true>(X, m, k, ldx, Q, scales, s);
+  if (k <= 8192) return launch_rows<uint16_t, 4, true>(X, m, k, ldx, Q, scales, s);
+  if (k <= 16384) return launch_rows<uint16_t, 8, true>(X, m, k, ldx, Q, scales, s);
+  return launch_rows<uint16_t, 1, false>(X, m, k, ldx, Q, scales, s);
+}
+
+hipError_t launch_i8_dequant(const WView& w, uint16_t* out, hipStream_t s) {
+  hipLaunchKernelGGL(k_i8_dequant, dim3((unsigned)w.n), dim3(kThreads), 0, s,
+                     reinterpret_cast<const int8_t*>(w.packed), w.scales, (int)w.k, out);
+  return hipGetLastError();
+}
+
+}  // namespace lbq

@@ -83,6 +83,9 @@ const lbq::Nf4Table& nf4_table() {
 // ---- validation ------------------------------------------------------------
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Longest row of 8-bit codes: 127 * 127 * 2^17 is below 2^31.
+constexpr int64_t kI8MaxK = int64_t(1) << 17;
+
 lbq_status check_desc(const lbq_desc* d) {
   if (d == nullptr) return fail(LBQ_E_NULL, "desc is NULL");
   if (d->format == LBQ_MINMAX) {
@@ -100,12 +103,20 @@ lbq_status check_desc(const lbq_desc* d) {
     if (d->double_quant < 0 || d->double_quant > 2)
       return fail(LBQ_E_FORMAT, "double_quant must be 0, 1 or 2 (with an offset), got %d", d->double_quant);
     if (d->dq_block != (d->double_quant ? 256 : 0)) return fail(LBQ_E_FORMAT, "dq_block must be 256 with double quantization and 0 otherwise");
+  } else if (d->format == LBQ_INT8) {
+    if (d->bits != 8) return fail(LBQ_E_FORMAT, "INT8 bits must be 8 (got %d)", d->bits);
+    if (d->group != 0) return fail(LBQ_E_FORMAT, "INT8 takes group = 0 (one scale per row), got %d", d->group);
+    if (d->double_quant != 0 || d->dq_block != 0) return fail(LBQ_E_FORMAT, "INT8 takes no double quantization");
+    if (d->meta != 0) return fail(LBQ_E_FORMAT, "INT8 takes meta = 0");
   } else {
-    return fail(LBQ_E_FORMAT, "unknown format %d (MINMAX=0, NF4=1)", d->format);
+    return fail(LBQ_E_FORMAT, "unknown format %d (MINMAX=0, NF4=1, INT8=2)", d->format);
   }
   if (d->n < 1 || d->n > (int64_t(1) << 31) - 1) return fail(LBQ_E_SHAPE, "n must be in [1, 2^31) (got %lld)", (long long)d->n);
   if (d->k < 64 || d->k > (int64_t(1) << 24)) return fail(LBQ_E_SHAPE, "k must be in [64, 2^24] (got %lld)", (long long)d->k);
-  if (d->k % 64 != 0 || d->k % d->group != 0) return fail(LBQ_E_SHAPE, "k (%lld) must be a multiple of 64 and of the group", (long long)d->k);
+  if (d->format == LBQ_INT8) {
+    if (d->k % 64 != 0 || d->k > kI8MaxK)
+      return fail(LBQ_E_SHAPE, "INT8 needs k (%lld) a multiple of 64 and at most %lld", (long long)d->k, (long long)kI8MaxK);
+  } else if (d->k % 64 != 0 || d->k % d->group != 0) return fail(LBQ_E_SHAPE, "k (%lld) must be a multiple of 64 and of the group", (long long)d->k);
   if (d->n * d->k > (int64_t(1) << 40)) return fail(LBQ_E_SHAPE, "n*k too large");
   if (d->format == LBQ_MINMAX && d->meta == LBQ_META_COMPACT && (d->k / d->group) * d->bits % 8 != 0)
     return fail(LBQ_E_SHAPE, "compact metadata needs (k / group) * bits %% 8 == 0 (k %lld)", (long long)d->k);
@@ -113,6 +124,7 @@ lbq_status check_desc(const lbq_desc* d) {
 }
 
 lbq::WKind kind_of(const lbq_desc* d) {
+  if (d->format == LBQ_INT8) return lbq::WK_I8;
   if (d->format == LBQ_NF4)
     return d->double_quant == 2 ? lbq::WK_NF4DQO : (d->double_quant ? lbq::WK_NF4DQ : lbq::WK_NF4);
   if (d->meta == LBQ_META_COMPACT) return d->bits == 4 ? lbq::WK_I4G128C : lbq::WK_I2G64C;
@@ -130,7 +142,9 @@ static_assert(sizeof(lbq_desc) == 40, "blob layout assumes a 40-byte descriptor"
 void sizes_of(const lbq_desc* d, lbq_sizes* s) {
   std::memset(s, 0, sizeof *s);
   s->packed = (size_t)(d->n * d->k * d->bits / 8);
-  if (d->format == LBQ_MINMAX) {
+  if (d->format == LBQ_INT8) {
+    s->scales = (size_t)d->n * sizeof(float);
+  } else if (d->format == LBQ_MINMAX) {
     const int64_t ng = d->n * (d->k / d->group);
     if (d->meta == LBQ_META_COMPACT) {
       s->scales = (size_t)ng * 2;                 // fp16
@@ -156,7 +170,10 @@ lbq_status check_qtensor(const lbq_desc* d, const lbq_qtensor* q) {
   if (q == nullptr) return fail(LBQ_E_NULL, "qtensor is NULL");
   if (q->packed == nullptr) return fail(LBQ_E_NULL, "qtensor.packed is NULL");
   if (!aligned(q->packed, 16)) return fail(LBQ_E_ALIGN, "qtensor.packed must be 16-byte aligned");
-  if (d->format == LBQ_MINMAX) {
+  if (d->format == LBQ_INT8) {
+    if (q->scales == nullptr) return fail(LBQ_E_NULL, "INT8 needs scales");
+    if (!aligned(q->scales, 4)) return fail(LBQ_E_ALIGN, "scales must be 4-byte aligned");
+  } else if (d->format == LBQ_MINMAX) {
     if (q->scales == nullptr || q->zeros == nullptr) return fail(LBQ_E_NULL, "MINMAX needs scales and zeros");
     if (!aligned(q->scales, d->meta == LBQ_META_COMPACT ? 2 : 4))
       return fail(LBQ_E_ALIGN, "scales must be 4-byte (fp32) or 2-byte (fp16) aligned");
@@ -183,6 +200,14 @@ lbq::WView view_of(const lbq_desc* d, const lbq_qtensor* q) {
   return w;
 }
 
+// The 8-bit kernels address a weight with 31-bit byte offsets (plus one tile
+// of slack past the last row).
+lbq_status check_i8_size(const lbq_desc* d) {
+  if (d->format == LBQ_INT8 && (uint64_t)(d->n + 256) * (uint64_t)d->k >= (uint64_t(1) << 31))
+    return fail(LBQ_E_SHAPE, "(n + 256) * k must be below 2^31 for INT8 (n %lld, k %lld)", (long long)d->n, (long long)d->k);
+  return LBQ_OK;
+}
+
 lbq_status check_fwd_common(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X,
                             int64_t m, uint16_t* Y, int64_t ldy) {
   lbq_status st = check_desc(desc);
@@ -196,6 +221,7 @@ lbq_status check_fwd_common(const lbq_desc* desc, const lbq_qtensor* q, const ui
       (uint64_t)(desc->n + 256) * (uint64_t)desc->k >= (uint64_t(1) << 32))
     return fail(LBQ_E_SHAPE, "(m + 256) * k * 2 and (n + 256) * k must be below 2^32 (m %lld, n %lld, k %lld)",
                 (long long)m, (long long)desc->n, (long long)desc->k);
+  if ((st = check_i8_size(desc)) != LBQ_OK) return st;
   if (X == nullptr || Y == nullptr) return fail(LBQ_E_NULL, "X and Y must be non-NULL");
   if (!aligned(X, 16)) return fail(LBQ_E_ALIGN, "X must be 16-byte aligned");
   if (!aligned(Y, 2)) return fail(LBQ_E_ALIGN, "Y must be 2-byte aligned");
@@ -219,6 +245,7 @@ int64_t round_rows(int64_t m) { return (m + 31) / 32 * 32; }
 // 23.6 us; q+k+v and o stay faster on the GEMV).  Decided per weight, so a
 // grouped call serves each weight as the single-weight call does.
 bool use_gemvm(const lbq_desc* d, int64_t m) {
+  if (d->format == LBQ_INT8) return false;  // its forward is i8_fwd
   if (!lbq::gemvm_fits(kind_of(d), d->k, m)) return false;
   return m < 3 || !lbq::skinny_fills_unsplit(d->n, d->k, m);
 }
@@ -232,10 +259,31 @@ float* gemm_part(const int64_t* ns, int count, int64_t k, int64_t m, void* ws, s
   return static_cast<float*>(ws);
 }
 
+size_t align16(size_t b) { return (b + 15) / 16 * 16; }
+
+// Workspace of the forward of INT8 weights that share X (16-byte aligned
+// pieces): the tokens' codes [m][k] and scales [m], then what the product
+// takes.
+size_t i8_token_bytes(int64_t m, int64_t k) { return align16((size_t)m * (size_t)k) + align16((size_t)m * sizeof(float)); }
+size_t i8_workspace(const int64_t* ns, int count, int64_t k, int64_t m) {
+  return i8_token_bytes(m, k) + lbq::i8_fwd_workspace_bytes(ns, count, k, m);
+}
+hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* rows, int count,
+                  const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, void* ws, hipStream_t s) {
+  const int64_t k = w[0].k;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  int8_t* xq = reinterpret_cast<int8_t*>(p);
+  float* xs = reinterpret_cast<float*>(p + align16((size_t)m * (size_t)k));
+  const hipError_t e = lbq::launch_i8_quant_bf16(X, m, k, k, xq, xs, s);
+  if (e != hipSuccess) return e;
+  return lbq::launch_i8_fwd(w, ys, ldys, rows, count, xq, xs, m, lora, p + i8_token_bytes(m, k), s);
+}
+
 hipError_t dispatch_fwd(const lbq_desc* desc, const lbq::WView& w, const uint16_t* X, int64_t m,
                         uint16_t* Y, int64_t ldy, const int32_t* out_rows,
                         const lbq::LoraEpi& lora, void* ws, size_t ws_bytes, hipStream_t s) {
   const lbq::WKind kind = kind_of(desc);
+  if (kind == lbq::WK_I8) return i8_fwd(&w, &Y, &ldy, &out_rows, 1, X, m, lora, ws, s);
   if (m == 1) return lbq::launch_gemv1(kind, &w, &Y, &out_rows, 1, X, lora, nf4_table(), s);
   if (use_gemvm(desc, m)) return lbq::launch_gemvm(kind, &w, &Y, &ldy, &out_rows, 1, X, m, lora, nf4_table(), s);
   if (m <= lbq::kSkinnyMaxM)
@@ -249,6 +297,7 @@ hipError_t dispatch_fwd(const lbq_desc* desc, const lbq::WView& w, const uint16_
 // Workspace of the forward: the small-batch kernel's partials (required) or,
 // for m > kSkinnyMaxM, the GEMM's K-split partials (optional).
 size_t fwd_workspace(const lbq_desc* desc, int64_t m, bool lora) {
+  if (desc->format == LBQ_INT8) return i8_workspace(&desc->n, 1, desc->k, m);
   if (use_gemvm(desc, m)) return 0;
   if (m >= 2 && m <= lbq::kSkinnyMaxM) return lbq::skinny_workspace_bytes(desc->n, desc->k, m, lora);
   if (m > lbq::kSkinnyMaxM) {
@@ -275,7 +324,7 @@ lbq_status check_bwd_common(const lbq_desc* desc, const lbq_qtensor* q, const ui
       (uint64_t)(desc->n + 256) * (uint64_t)desc->k >= (uint64_t(1) << 32))
     return fail(LBQ_E_SHAPE, "(m + 256) * n * 2, (m + 256) * k * 2 and (n + 256) * k must be below 2^32 "
                 "(m %lld, n %lld, k %lld)", (long long)m, (long long)desc->n, (long long)desc->k);
-  return LBQ_OK;
+  return check_i8_size(desc);
 }
 
 }  // namespace
@@ -298,7 +347,8 @@ lbq_status linear_fwd_body(const lbq_desc* desc, const lbq_qtensor* q, const uin
                            const char* who) {
   if (m == 0) return ok();
   const size_t need = fwd_workspace(desc, m, false);
-  if (m <= lbq::kSkinnyMaxM && need > 0) {  // the GEMM's partials are optional
+  // the partials of the m > 64 GEMM are optional
+  if ((m <= lbq::kSkinnyMaxM || desc->format == LBQ_INT8) && need > 0) {
     if (workspace == nullptr || ws_bytes < need)
       return fail(LBQ_E_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws_bytes);
     if (!aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
@@ -329,7 +379,9 @@ lbq_status lbq_quantize(const lbq_desc* desc, const float* W, const lbq_qtensor*
   if (!aligned(W, 16)) return fail(LBQ_E_ALIGN, "W must be 16-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
-  if (desc->format == LBQ_MINMAX) {
+  if (desc->format == LBQ_INT8) {
+    e = lbq::launch_i8_quant_f32(W, desc->n, desc->k, static_cast<int8_t*>(q->packed), static_cast<float*>(q->scales), s);
+  } else if (desc->format == LBQ_MINMAX) {
     e = lbq::launch_quant_minmax(desc->bits, desc->group, desc->meta == LBQ_META_COMPACT, W,
                                  static_cast<uint8_t*>(q->packed), static_cast<float*>(q->scales), q->zeros,
                                  desc->n, desc->k, s);
@@ -347,6 +399,8 @@ lbq_status lbq_dequant(const lbq_desc* desc, const lbq_qtensor* q, uint16_t* W_b
   if ((st = check_qtensor(desc, q)) != LBQ_OK) return st;
   if (W_bf16 == nullptr) return fail(LBQ_E_NULL, "W_bf16 is NULL");
   if (!aligned(W_bf16, 16)) return fail(LBQ_E_ALIGN, "W_bf16 must be 16-byte aligned");
+  if (desc->format == LBQ_INT8)
+    return hip_status(lbq::launch_i8_dequant(view_of(desc, q), W_bf16, static_cast<hipStream_t>(stream)), "lbq_dequant");
   return hip_status(lbq::launch_dequant(kind_of(desc), view_of(desc, q), W_bf16, nf4_table(),
                                         static_cast<hipStream_t>(stream)),
                     "lbq_dequant");
@@ -363,6 +417,47 @@ lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint
   const lbq_status st = check_fwd_common(desc, q, X, m, Y, ldy);
   if (st != LBQ_OK) return st;
   return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, workspace, ws_bytes, stream, "lbq_linear_fwd");
+}
+
+lbq_status lbq_quantize_tokens(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Xq, float* xscale,
+                               void* stream) {
+  if (m < 0 || m > (int64_t(1) << 31) - 1) return fail(LBQ_E_SHAPE, "m must be in [0, 2^31) (got %lld)", (long long)m);
+  if (k < 64 || k > kI8MaxK || k % 64 != 0)
+    return fail(LBQ_E_SHAPE, "k must be a multiple of 64 in [64, %lld] (got %lld)", (long long)kI8MaxK, (long long)k);
+  if (ldx < k) return fail(LBQ_E_SHAPE, "ldx (%lld) < k (%lld)", (long long)ldx, (long long)k);
+  if (ldx % 8 != 0) return fail(LBQ_E_ALIGN, "ldx must be a multiple of 8 (got %lld)", (long long)ldx);
+  if (m == 0) return ok();
+  if (X == nullptr || Xq == nullptr || xscale == nullptr) return fail(LBQ_E_NULL, "X, Xq and xscale must be non-NULL");
+  if (!aligned(X, 16) || !aligned(Xq, 16)) return fail(LBQ_E_ALIGN, "X and Xq must be 16-byte aligned");
+  if (!aligned(xscale, 4)) return fail(LBQ_E_ALIGN, "xscale must be 4-byte aligned");
+  return hip_status(lbq::launch_i8_quant_bf16(X, m, k, ldx, Xq, xscale, static_cast<hipStream_t>(stream)),
+                    "lbq_quantize_tokens");
+}
+
+size_t lbq_linear_fwd_tokens_workspace_bytes(const lbq_desc* desc, int64_t m) {
+  if (check_desc(desc) != LBQ_OK || desc->format != LBQ_INT8 || m < 1) return 0;
+  return lbq::i8_fwd_workspace_bytes(&desc->n, 1, desc->k, m);
+}
+
+lbq_status lbq_linear_fwd_tokens(const lbq_desc* desc, const lbq_qtensor* q, const int8_t* Xq, const float* xscale,
+                                 int64_t m, uint16_t* Y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
+  lbq_status st = check_fwd_common(desc, q, reinterpret_cast<const uint16_t*>(Xq), m, Y, ldy);
+  if (st != LBQ_OK) return st;
+  if (desc->format != LBQ_INT8) return fail(LBQ_E_UNSUPPORTED, "lbq_linear_fwd_tokens takes INT8 weights");
+  if (m == 0) return ok();
+  if (xscale == nullptr) return fail(LBQ_E_NULL, "xscale must be non-NULL");
+  if (!aligned(xscale, 4)) return fail(LBQ_E_ALIGN, "xscale must be 4-byte aligned");
+  const size_t need = lbq::i8_fwd_workspace_bytes(&desc->n, 1, desc->k, m);
+  if (need > 0) {
+    if (workspace == nullptr || ws_bytes < need)
+      return fail(LBQ_E_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws_bytes);
+    if (!aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
+  }
+  const lbq::LoraEpi none{nullptr, nullptr, 0, 0};
+  const lbq::WView w = view_of(desc, q);
+  return hip_status(lbq::launch_i8_fwd(&w, &Y, &ldy, &q->out_rows, 1, Xq, xscale, m, none, workspace,
+                                       static_cast<hipStream_t>(stream)),
+                    "lbq_linear_fwd_tokens");
 }
 
 // A grouped call at 2 <= m <= 64 whose weights are all INT4 g128 or INT2 g64,
@@ -400,6 +495,15 @@ static bool gemvm_mix_set(int32_t count, const lbq_desc* descs, int64_t m) {
   return ca > 0 && cb > 0;
 }
 
+// Workspace of the INT8 weights of a grouped call, 0 when it has none.
+static size_t grouped_i8_workspace(int32_t count, const lbq_desc* descs, int64_t m) {
+  int64_t ns[LBQ_MAX_GROUP];
+  int c = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (descs[i].format == LBQ_INT8) ns[c++] = descs[i].n;
+  return c > 0 ? i8_workspace(ns, c, descs[0].k, m) : 0;
+}
+
 // Weights of one kind in a grouped call run as one launch (one launch pair
 // for the small-batch kernel when it splits K, and up to two GEMM launches
 // when splitting the set fills the chip better), one kind after another on
@@ -409,9 +513,12 @@ size_t lbq_linear_fwd_grouped_workspace_bytes(int32_t count, const lbq_desc* des
   if (count < 1 || count > LBQ_MAX_GROUP || descs == nullptr) return 0;
   for (int32_t i = 0; i < count; ++i)
     if (check_desc(&descs[i]) != LBQ_OK || descs[i].k != descs[0].k) return 0;
+  if (m < 1) return 0;
+  const size_t i8 = grouped_i8_workspace(count, descs, m);
+  bool done[LBQ_MAX_GROUP] = {};
+  for (int32_t i = 0; i < count; ++i) done[i] = descs[i].format == LBQ_INT8;
   if (m > lbq::kSkinnyMaxM) {  // the GEMM's K-split partials, per kind group
-    size_t need = 0;
-    bool done[LBQ_MAX_GROUP] = {};
+    size_t need = i8;
     for (int32_t i = 0; i < count; ++i) {
       if (done[i]) continue;
       int64_t ns[LBQ_MAX_GROUP];
@@ -425,14 +532,13 @@ size_t lbq_linear_fwd_grouped_workspace_bytes(int32_t count, const lbq_desc* des
     }
     return need;
   }
-  if (m < 2) return 0;
+  if (m < 2) return i8;
   if (skinny_mix_set(count, descs, m)) {
     int64_t ns[LBQ_MAX_GROUP];
     for (int32_t i = 0; i < count; ++i) ns[i] = descs[i].n;
     return lbq::skinny_set_workspace_bytes(ns, count, descs[0].k, m);
   }
-  size_t need = 0;
-  bool done[LBQ_MAX_GROUP] = {};
+  size_t need = i8;
   for (int32_t i = 0; i < count; ++i) {
     if (done[i]) continue;
     const lbq::WKind kind = kind_of(&descs[i]);
@@ -464,8 +570,10 @@ lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lb
                   (long long)descs[0].k);
   }
   if (m == 0) return ok();
-  const size_t need = lbq_linear_fwd_grouped_workspace_bytes(count, descs, m);
-  if (m <= lbq::kSkinnyMaxM && need > 0) {  // the GEMM's partials are optional
+  // the partials of the m > 64 GEMM are optional, what INT8 weights take is not
+  const size_t need = m <= lbq::kSkinnyMaxM ? lbq_linear_fwd_grouped_workspace_bytes(count, descs, m)
+                                            : grouped_i8_workspace(count, descs, m);
+  if (need > 0) {
     if (workspace == nullptr || ws_bytes < need)
       return fail(LBQ_E_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws_bytes);
     if (!aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
@@ -526,7 +634,8 @@ lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lb
       rows[c] = qs[j].out_rows;
       ++c;
     }
-    if (m == 1) e = lbq::launch_gemv1(kind, ws, ys, rows, c, X, none, nf4_table(), s);
+    if (kind == lbq::WK_I8) e = i8_fwd(ws, ys, lds, rows, c, X, m, none, workspace, s);
+    else if (m == 1) e = lbq::launch_gemv1(kind, ws, ys, rows, c, X, none, nf4_table(), s);
     else if (gemvm) e = lbq::launch_gemvm(kind, ws, ys, lds, rows, c, X, m, none, nf4_table(), s);
     else if (m <= lbq::kSkinnyMaxM)
       e = lbq::launch_skinny_set(kind, ws, ys, lds, rows, c, X, m, static_cast<float*>(workspace), nf4_table(), s);
@@ -571,11 +680,6 @@ lbq_status lbq_linear_bwd_dx_grouped(int32_t count, const lbq_desc* descs, const
                                            static_cast<hipStream_t>(stream)),
                     "lbq_linear_bwd_dx_grouped");
 }
-
-// LoRA backward workspace (16-byte aligned pieces): Bt = B^T [rp][n] bf16,
-// G = bf16(sigma dY B) [m][rp], T = bf16(sigma X A^T) [m][rp], then the fp32
-// partial sums of the dA / dB reductions (reused by both).
-static size_t align16(size_t b) { return (b + 15) / 16 * 16; }
 
 // LoRA backward workspace: Bt [rp][n], G [m][rp], Gt and Tt [rp][mp] (bf16),
 // then fp32 partial sums shared by the four reductions (they run in turn).
@@ -688,6 +792,103 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
   const lbq::WView w = view_of(desc, q);
   return hip_status(dispatch_fwd(desc, w, X, m, Y, ldy, q->out_rows, lora, part, ws_bytes - lora_t_bytes(m, r), s),
                     "lbq_lora_fwd");
+}
+
+// ---- gradient norm and clipping --------------------------------------------
+
+// Checks of a list of gradients; with `write`, of where the scaled ones go.
+static lbq_status check_grads(int32_t count, const lbq_grad* g, bool write) {
+  if (count < 1) return fail(LBQ_E_SHAPE, "count must be at least 1 (got %d)", count);
+  if (g == nullptr) return fail(LBQ_E_NULL, "grads must be non-NULL");
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].dtype != LBQ_F32 && g[i].dtype != LBQ_BF16 && g[i].dtype != LBQ_F16)
+      return fail(LBQ_E_FORMAT, "grads[%d].dtype must be 0 (fp32), 1 (bf16) or 2 (fp16), got %d", i, g[i].dtype);
+    if (g[i].numel < 0 || (total += g[i].numel) > (int64_t(1) << 40))
+      return fail(LBQ_E_SHAPE, "numel must be at least 0 and 2^40 in all (grads[%d] has %lld)", i, (long long)g[i].numel);
+    if (g[i].numel == 0) continue;
+    const size_t size = g[i].dtype == LBQ_F32 ? 4 : 2;
+    if (g[i].grad == nullptr || (write && g[i].out == nullptr))
+      return fail(LBQ_E_NULL, "grads[%d] has a NULL pointer", i);
+    if (!aligned(g[i].grad, size) || (write && !aligned(g[i].out, size)))
+      return fail(LBQ_E_ALIGN, "grads[%d] must be aligned to its type", i);
+  }
+  return LBQ_OK;
+}
+
+// Whether a tensor that is written overlaps another one's memory: the memory
+// ranges in the order of their addresses, each against the furthest end so far.
+static bool grads_overlap(int32_t count, const lbq_grad* g) {
+  struct Range {
+    uintptr_t lo, hi;
+    bool write;
+  };
+  std::vector<Range> r;
+  r.reserve(2 * (size_t)count);
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    const uintptr_t bytes = (uintptr_t)g[i].numel * (g[i].dtype == LBQ_F32 ? 4 : 2);
+    const uintptr_t in = reinterpret_cast<uintptr_t>(g[i].grad), out = reinterpret_cast<uintptr_t>(g[i].out);
+    r.push_back({out, out + bytes, true});
+    if (in != out) r.push_back({in, in + bytes, false});
+  }
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, written = 0;
+  for (const Range& x : r) {
+    if (x.lo < (x.write ? end : written)) return true;
+    end = std::max(end, x.hi);
+    if (x.write) written = std::max(written, x.hi);
+  }
+  return false;
+}
+
+size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads) {
+  if (check_grads(count, grads, false) != LBQ_OK) return 0;
+  return align16((size_t)lbq::grad_parts(grads, count) * sizeof(double));
+}
+
+static lbq_status grad_body(int32_t count, const lbq_grad* grads, int32_t norm_type, const float* max_norm, float* norm,
+                            void* workspace, size_t ws_bytes, void* stream, const char* who) {
+  lbq_status st = check_grads(count, grads, max_norm != nullptr);
+  if (st != LBQ_OK) return st;
+  if (norm_type != LBQ_NORM_2 && norm_type != LBQ_NORM_INF)
+    return fail(LBQ_E_FORMAT, "norm_type must be 0 (2-norm) or 1 (largest magnitude), got %d", norm_type);
+  if (norm == nullptr) return fail(LBQ_E_NULL, "norm must be non-NULL");
+  if (!aligned(norm, 4)) return fail(LBQ_E_ALIGN, "norm must be 4-byte aligned");
+  if (max_norm != nullptr) {
+    if (!std::isfinite(*max_norm) || !(*max_norm > 0.f)) return fail(LBQ_E_SHAPE, "max_norm must be finite and positive");
+    try {
+      if (grads_overlap(count, grads)) return fail(LBQ_E_SHAPE, "a scaled gradient overlaps another tensor of the call");
+    } catch (...) {
+      return fail(LBQ_E_WORKSPACE, "%s: out of host memory", who);
+    }
+  }
+  const int parts = lbq::grad_parts(grads, count);
+  const size_t need = align16((size_t)parts * sizeof(double));
+  if (need > 0) {
+    if (workspace == nullptr || ws_bytes < need)
+      return fail(LBQ_E_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws_bytes);
+    if (!aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
+  }
+  const bool inf = norm_type == LBQ_NORM_INF;
+  double* part = static_cast<double*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = parts > 0 ? lbq::launch_grad_norm(grads, count, inf, part, s) : hipSuccess;
+  if (e == hipSuccess) {
+    if (max_norm != nullptr && parts > 0) e = lbq::launch_grad_scale(grads, count, inf, part, parts, *max_norm, norm, s);
+    else e = lbq::launch_grad_norm_out(inf, part, parts, norm, s);
+  }
+  return hip_status(e, who);
+}
+
+lbq_status lbq_grad_norm(int32_t count, const lbq_grad* grads, int32_t norm_type, float* norm, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  return grad_body(count, grads, norm_type, nullptr, norm, workspace, ws_bytes, stream, "lbq_grad_norm");
+}
+
+lbq_status lbq_clip_grads(int32_t count, const lbq_grad* grads, int32_t norm_type, float max_norm, float* norm,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  return grad_body(count, grads, norm_type, &max_norm, norm, workspace, ws_bytes, stream, "lbq_clip_grads");
 }
 
 // ---- serialization --------------------------------------------------------

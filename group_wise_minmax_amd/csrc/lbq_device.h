@@ -139,6 +139,8 @@ template <> struct WKindTraits<WK_I4G128C> { static constexpr int fmt = FMT_MINM
 template <> struct WKindTraits<WK_I2G64C>  { static constexpr int fmt = FMT_MINMAX, bits = 2, group = 64;  static constexpr bool dq = false, compact = true,  dqo = false; };
 template <> struct WKindTraits<WK_NF4DQO>  { static constexpr int fmt = FMT_NF4,    bits = 4, group = 64;  static constexpr bool dq = true,  compact = false, dqo = true; };
 
+template <> struct WKindTraits<WK_I8>      { static constexpr int fmt = FMT_INT8,   bits = 8, group = 0;   static constexpr bool dq = false, compact = false, dqo = false; };
+
 // fp16 bit pattern -> its exact fp32 value (normal and subnormal; no NaN/Inf
 // in the contract).  One v_cvt_f32_f16: every fp16 value, subnormals
 // included, is a normal fp32 number, and fp16 denormals are kept by the
@@ -298,7 +300,11 @@ __device__ __forceinline__ float nf4_block_scale(const WView& w, int64_t blk, fl
   }
 }
 
-// Dispatch a functor templated on the weight kind.
+// bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
+__device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
+
+// Dispatch a functor templated on the weight kind (the group-wise formats and
+// NF4; 8-bit rows have kernels of their own and an input-gradient variant).
 template <template <int> class F, typename... Args>
 hipError_t dispatch_kind(WKind kind, Args&&... args) {
   switch (kind) {
@@ -311,6 +317,7 @@ hipError_t dispatch_kind(WKind kind, Args&&... args) {
     case WK_I4G128C: return F<WK_I4G128C>::run(args...);
     case WK_I2G64C: return F<WK_I2G64C>::run(args...);
     case WK_NF4DQO: return F<WK_NF4DQO>::run(args...);
+    case WK_I8: break;
   }
   return hipErrorInvalidValue;
 }

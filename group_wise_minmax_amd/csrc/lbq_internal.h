@@ -5,9 +5,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lbq.h"
+
 namespace lbq {
 
-enum Fmt : int { FMT_MINMAX = 0, FMT_NF4 = 1 };
+enum Fmt : int { FMT_MINMAX = 0, FMT_NF4 = 1, FMT_INT8 = 2 };
 
 // One quantized weight as the kernels see it (device pointers + shape).
 // `scales` holds fp32 values, or fp16 bit patterns under compact metadata.
@@ -55,6 +57,7 @@ enum WKind : int {
   WK_I4G128C = 6, // MinMax 4-bit, group 128, compact metadata (fp16 scale, packed zero)
   WK_I2G64C = 7,  // MinMax 2-bit, group 64, compact metadata
   WK_NF4DQO = 8,  // NF4, block 64, double quant with a per-tensor offset
+  WK_I8 = 9,      // symmetric 8-bit, one scale per row (k_i8_*.hip, k_bwd.hip)
 };
 
 // ---- launchers (each returns hipGetLastError() after the launch) ----------
@@ -169,6 +172,51 @@ hipError_t launch_lora_outer_jobs(int count, const uint16_t* const* Pts, const u
                                   int32_t r, int64_t m, float* part, hipStream_t s);
 hipError_t launch_fill_zero_f32(float* p, int64_t count, hipStream_t s);
 
+// ---- 8-bit weights (WK_I8) and tokens ----------------------------------------
+// Rows to 8-bit codes and one fp32 scale each: W [n][k] fp32, or X [m][ldx]
+// bf16 of which k columns are used (k % 8 == 0, 16-byte aligned rows).
+hipError_t launch_i8_quant_f32(const float* W, int64_t n, int64_t k, int8_t* Q, float* scales, hipStream_t s);
+hipError_t launch_i8_quant_bf16(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Q, float* scales,
+                                hipStream_t s);
+hipError_t launch_i8_dequant(const WView& w, uint16_t* out, hipStream_t s);
+// Weights that multiply the same tokens in one launch.
+struct I8Set {
+  const int8_t* w[kGemvMaxGroup];
+  const float* ws[kGemvMaxGroup];
+  uint16_t* y[kGemvMaxGroup];
+  const int32_t* rows[kGemvMaxGroup];  // out_rows, or nullptr
+  int64_t ldy[kGemvMaxGroup];
+  int n[kGemvMaxGroup];
+  int tile_end[kGemvMaxGroup];  // weight i owns the row tiles [tile_end[i-1], tile_end[i])
+  int count;
+};
+// The product on quantized tokens Xq [m][k] with scales xs [m], for up to
+// kGemvMaxGroup weights of one k (the LoRA term only with count 1).  `work`
+// holds i8_fwd_workspace_bytes() bytes.
+size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m);
+hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows,
+                         int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void* work,
+                         hipStream_t s);
+
+// ---- gradient norm (k_grad.hip) -------------------------------------------------
+// Tensors of one launch, in the kernel's arguments (they may take 4 KiB).
+constexpr int kGradTable = 120;
+struct GradTable {
+  const void* grad[kGradTable];
+  void* out[kGradTable];
+  int64_t numel[kGradTable];
+  int piece_end[kGradTable];
+  uint8_t dtype[kGradTable];
+  int count;
+};
+constexpr int kGradGroups = 2048;  // workgroups over all the launches of one pass (a few more when there are many)
+int64_t grad_pieces(const lbq_grad* g, int count);
+int grad_parts(const lbq_grad* g, int count);
+hipError_t launch_grad_norm(const lbq_grad* g, int count, bool inf, double* part, hipStream_t s);
+hipError_t launch_grad_norm_out(bool inf, const double* part, int parts, float* norm, hipStream_t s);
+hipError_t launch_grad_scale(const lbq_grad* g, int count, bool inf, const double* part, int parts, float max_norm,
+                             float* norm, hipStream_t s);
+
 // Largest m served by the small-batch MFMA kernel.
 constexpr int64_t kSkinnyMaxM = 64;
 
@@ -176,8 +224,6 @@ constexpr int64_t kSkinnyMaxM = 64;
 
 // C-ABI helpers shared between lbq_api.cpp and the allocation-free forward
 // (k_noalloc.hip); the types come from include/lbq.h.
-#include "lbq.h"
-
 namespace lbq {
 
 // Records `what` as the detail of the calling thread's last failure; returns s.

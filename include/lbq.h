@@ -64,7 +64,8 @@ typedef enum {
 
 typedef enum {
   LBQ_MINMAX = 0, /* asymmetric group-wise MinMax RTN [GB]                   */
-  LBQ_NF4 = 1     /* 4-bit NormalFloat, blockwise absmax, optional DQ [QL]   */
+  LBQ_NF4 = 1,    /* 4-bit NormalFloat, blockwise absmax, optional DQ [QL]   */
+  LBQ_INT8 = 2    /* symmetric 8-bit integers, one scale per output channel  */
 } lbq_format;
 
 /* MinMax metadata layouts (lbq_desc.meta). */
@@ -83,6 +84,9 @@ typedef enum {
  *           (fp32 absmax), 1 (absmax double-quantized) or 2 (double-quantized
  *           with a per-tensor offset); dq_block = 256 with double
  *           quantization, else 0.
+ *   INT8:   bits = 8, group = 0 (one scale for a whole row); double_quant =
+ *           dq_block = meta = 0; k % 64 == 0, k <= 2^17 (the integer sums of
+ *           a product stay below 2^31).
  * n >= 1, k >= 64. */
 typedef struct {
   int32_t format;
@@ -99,10 +103,12 @@ typedef struct {
  *   packed        all formats  u8[n][k*bits/8]; 4-bit: byte i of a row holds
  *                              code 2i in bits 7..4 and code 2i+1 in bits 3..0
  *                              [BNB]; 2-bit: code 4i in bits 7..6, then 5..4,
- *                              3..2, 1..0.  Only the bytes matter: the caller
+ *                              3..2, 1..0; INT8: i8[n][k], the codes
+ *                              themselves.  Only the bytes matter: the caller
  *                              may hold them in any dtype of the same size.
  *   scales        MINMAX       f32[n][k/group]; compact: fp16 bit patterns
  *                              u16[n][k/group] (2-byte aligned)
+ *                 INT8         f32[n]
  *   zeros         MINMAX       u8 [n][k/group]  (integer zero point 0..2^bits-1);
  *                              compact: u8[n][(k/group)*bits/8], the zero
  *                              points of a row packed like the codes (first
@@ -161,6 +167,9 @@ lbq_status lbq_layout(const lbq_desc* desc, lbq_sizes* out);
  *     (zero-padded to a power of two, fp32 additions); per run of 256:
  *     d = fl(a - off), c2 = fl(max|d|/127), q2 = clamp(rne(fl(d/c2)), -127,
  *     127) (0 if c2 == 0); decoded as fl(fl(q2 * c2) + off).  Three launches.
+ *   INT8: per row: s = fl(max|w| / 127), s := 1 if it is 0;
+ *     q = clamp(rne(fl(w/s)), -127, 127).  A row that holds an infinity or a
+ *     NaN gets the scale NaN and codes 0.
  * Every fp32 step is one IEEE operation rounded to nearest-even (true
  * division, no contraction); results are bit-exact across runs.
  * Pure: it never inspects the old contents of the outputs. */
@@ -170,14 +179,16 @@ lbq_status lbq_quantize(const lbq_desc* desc, const float* W, const lbq_qtensor*
 /* Dequantize to bf16 W_bf16[n][k] (device) [BNB] 通过BitsAndBytesConfig配置:
  *   MINMAX: bf16(fl((q - z) * s));  NF4: bf16(fl(c[code] * A)) with A the block
  *   absmax, fl(q2 * c2) under double quantization, or fl(fl(q2 * c2) + off)
- *   with an offset.  bf16 rounding is round-to-nearest-even; the result is
- *   bit-exact. */
+ *   with an offset;  INT8: bf16(fl(q * s)).  bf16 rounding is
+ *   round-to-nearest-even; the result is bit-exact. */
 lbq_status lbq_dequant(const lbq_desc* desc, const lbq_qtensor* q, uint16_t* W_bf16,
                        void* stream);
 
 /* Workspace bytes lbq_linear_fwd takes for m rows (0 when none): for
  * 2 <= m <= 64 the small-batch kernel's partial sums (required); for m > 64
- * the partial sums of a GEMM that splits K (optional, see lbq_linear_fwd). */
+ * the partial sums of a GEMM that splits K (optional, see lbq_linear_fwd).
+ * For an INT8 weight the codes and scales of the tokens, and the partial sums
+ * of a kernel that splits K (required at every m where it is not 0). */
 size_t lbq_linear_workspace_bytes(const lbq_desc* desc, int64_t m);
 
 /* Forward of the frozen low-bit linear layer, Y = X . deq(W)^T ([BNB]
@@ -207,7 +218,10 @@ size_t lbq_linear_workspace_bytes(const lbq_desc* desc, int64_t m);
  * n > 13056 rows and k <= 4096, which takes the next kernel (faster there);
  * otherwise, up to m = 64, a bf16-MFMA kernel that streams the weight
  * once with K split over workgroups; larger m a bf16-MFMA GEMM whose weight
- * tiles are dequantized once into LDS. */
+ * tiles are dequantized once into LDS.
+ * An INT8 weight multiplies 8-bit tokens: each row of X is quantized as
+ * lbq_quantize_tokens does it and the product is that of
+ * lbq_linear_fwd_tokens, bit for bit; the workspace is required. */
 lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X,
                           int64_t m, uint16_t* Y, int64_t ldy, void* workspace,
                           size_t ws_bytes, void* stream);
@@ -235,6 +249,36 @@ lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint
  * race and must be serialized by the caller. */
 lbq_status lbq_linear_fwd_noalloc(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X,
                                   int64_t m, uint16_t* Y, int64_t ldy, void* stream);
+
+/* ---- 8-bit tokens and the product with INT8 weights ----------------------- */
+
+/* Quantize the rows of X (tokens) to 8-bit integers with one scale each, by
+ * the rule of lbq_quantize's INT8 format:
+ *   s = fl(max|x| / 127), s := 1 if it is 0; q = clamp(rne(fl(x/s)), -127, 127);
+ *   a row that holds an infinity or a NaN gets the scale NaN and codes 0, so
+ *   that its products are NaN and no other row's are.
+ * X: bf16, m rows of k values, ldx apart (ldx >= k, ldx % 8 == 0); Xq: i8
+ * [m][k]; xscale: f32 [m] (device).  X and Xq 16-byte aligned, xscale 4-byte
+ * aligned; 64 <= k <= 2^17, k % 64 == 0; m >= 0 (0: nothing is written). */
+lbq_status lbq_quantize_tokens(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Xq,
+                               float* xscale, void* stream);
+
+/* Workspace bytes lbq_linear_fwd_tokens takes for m rows (0 when none). */
+size_t lbq_linear_fwd_tokens_workspace_bytes(const lbq_desc* desc, int64_t m);
+
+/* Product of quantized tokens with an INT8 weight:
+ *   Y[i][col(j)] = bf16( fl(fl(fl(acc) * xscale[i]) * s[j]) ),
+ *   acc = sum_k Xq[i][k] * q[j][k],  col(j) as in lbq_linear_fwd,
+ * acc summed exactly in 32-bit integers (every m and n gives the same bits),
+ * fl() rounding to fp32.  desc->format must be LBQ_INT8 (LBQ_E_UNSUPPORTED
+ * otherwise); Xq: i8 [m][k] with values in [-127, 127], 16-byte aligned;
+ * xscale: f32 [m].  (m + 256) * k * 2 below 2^32 and (n + 256) * k below 2^31
+ * (LBQ_E_SHAPE otherwise).  `workspace` must hold
+ * lbq_linear_fwd_tokens_workspace_bytes(desc, m) bytes, 16-byte aligned (may
+ * be NULL when that is 0).  Y and ldy as in lbq_linear_fwd. */
+lbq_status lbq_linear_fwd_tokens(const lbq_desc* desc, const lbq_qtensor* q, const int8_t* Xq,
+                                 const float* xscale, int64_t m, uint16_t* Y, int64_t ldy, void* workspace,
+                                 size_t ws_bytes, void* stream);
 
 /* Largest count accepted by lbq_linear_fwd_grouped. */
 #define LBQ_MAX_GROUP 8
@@ -266,10 +310,12 @@ size_t lbq_linear_fwd_grouped_workspace_bytes(int32_t count, const lbq_desc* des
  * multi-row GEMV at 2 <= m <= 4 when every weight takes it, else the
  * small-batch kernel (and its reduce).  Each Ys[i] equals what lbq_linear_fwd
  * writes for weight i alone, bit for bit (given workspaces of the queried
- * sizes: each weight splits K as it does alone).  `workspace` takes
+ * sizes: each weight splits K as it does alone).  The INT8 weights of a set
+ * share one quantization of X.  `workspace` takes
  * lbq_linear_fwd_grouped_workspace_bytes(count, descs, m) bytes (16-byte
  * aligned; 0 for m == 1 and the multi-row GEMV): required for m <= 64,
- * optional for m > 64 as in lbq_linear_fwd. */
+ * optional for m > 64 as in lbq_linear_fwd; required whenever an INT8 weight
+ * is in the set. */
 lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
                                   const uint16_t* X, int64_t m, uint16_t* const* Ys,
                                   const int64_t* ldys, void* workspace, size_t ws_bytes,
@@ -280,7 +326,9 @@ lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lb
  *   dX[i][k] = bf16( sum_j dY[i][j] * w_hat[j][k] ), fp32 accumulation.
  * dY: bf16 [m][n]; dX: bf16 [m][k] (device), both 16-byte aligned; n % 8
  * == 0; (m + 256) * n * 2 and (n + 256) * k below 2^32 (LBQ_E_SHAPE
- * otherwise).  out_rows must be NULL (LBQ_E_UNSUPPORTED otherwise). */
+ * otherwise; INT8: (n + 256) * k below 2^31).  out_rows must be NULL
+ * (LBQ_E_UNSUPPORTED otherwise).  For an INT8 weight this is the gradient of
+ * the unrounded product: the rounding of the tokens passes it on unchanged. */
 lbq_status lbq_linear_bwd_dx(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* dY,
                              int64_t m, uint16_t* dX, void* stream);
 
@@ -333,6 +381,50 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
                         int64_t m, const uint16_t* A, const uint16_t* B, int32_t r,
                         float sigma, uint16_t* Y, int64_t ldy, void* workspace,
                         size_t ws_bytes, void* stream);
+
+/* ---- Gradient norm and clipping ------------------------------------------- */
+
+typedef enum { LBQ_F32 = 0, LBQ_BF16 = 1, LBQ_F16 = 2 } lbq_dtype;
+typedef enum { LBQ_NORM_2 = 0, LBQ_NORM_INF = 1 } lbq_norm;
+
+/* One gradient tensor: `numel` contiguous values of type lbq_dtype at `grad`
+ * (device), and where lbq_clip_grads writes them scaled: `out`, of the same
+ * type, the same pointer as `grad` (in place) or memory of its own.  Both are
+ * aligned to the type (16-byte aligned tensors run faster).  numel >= 0, at
+ * most 2^40; with numel 0 the pointers are not looked at. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype;
+  int32_t reserved; /* 0 */
+} lbq_grad;
+
+/* Workspace bytes the two calls below take. */
+size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads);
+
+/* Norm over all the values of `count` tensors (count >= 1; a tensor listed
+ * twice counts twice):
+ *   LBQ_NORM_2:   *norm = fp32( sqrt( sum x^2 ) ), the sum in fp64;
+ *   LBQ_NORM_INF: *norm = max |x|;
+ * a NaN among the values gives a NaN.  grads: host array; norm: one fp32
+ * (device).  `out` is not looked at.  Summed in a fixed order (run-to-run
+ * identical for the same sizes and alignments).  `workspace`:
+ * lbq_grad_workspace_bytes(count, grads) bytes, 16-byte aligned; every launch
+ * that overlaps another needs one of its own. */
+lbq_status lbq_grad_norm(int32_t count, const lbq_grad* grads, int32_t norm_type, float* norm, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* The norm as above, and every tensor scaled so that it is at most max_norm
+ * (the training loop's step between the backward pass and the optimizer,
+ * [QL] QLoRA技术原理: the gradients of the low-rank adapters):
+ *   c = min(1, fl(max_norm / fl(*norm + 1e-6))), out = round(x * c) in the
+ *   tensor's type.  A norm that is NaN makes every value NaN; an infinite one
+ *   makes c 0.  With c = 1 tensors that are scaled in place are not written.
+ * max_norm: finite and positive.  The outputs may overlap neither each other
+ * nor a gradient other than their own (LBQ_E_SHAPE otherwise). */
+lbq_status lbq_clip_grads(int32_t count, const lbq_grad* grads, int32_t norm_type, float max_norm, float* norm,
+                          void* workspace, size_t ws_bytes, void* stream);
 
 /* ---- Serialization ([BNB] 源码纵深: the state dict saves the 4-bit weight
  * together with its quantization-state fields so that the layer can be rebuilt
