@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t f16_rne(float f) {
 __device__ __forceinline__ uint32_t bf16_rne_nan(float f) { return f != f ? 0x7FC0u : bf16_rne(f); }
 
 // Combines the threads' values in a fixed order; the result in every thread.
-template <bool INF>
+template <bool INF, int NT>
 __device__ __forceinline__ double block_combine(double v) {
-  __shared__ double red[kThreads / 64];
+  __shared__ double red[NT / 64];
   if constexpr (INF) {
     // magnitudes are not negative: their bits order like the values, NaN last
     uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -58,7 +58,7 @@ __device__ __forceinline__ double block_combine(double v) {
   __syncthreads();
   double r = red[0];
 #pragma unroll
-  for (int i = 1; i < kThreads / 64; ++i) {
+  for (int i = 1; i < NT / 64; ++i) {
     if constexpr (INF) {
       const uint64_t a = __builtin_bit_cast(uint64_t, r), b = __builtin_bit_cast(uint64_t, red[i]);
       r = __builtin_bit_cast(double, b > a ? b : a);
@@ -80,68 +80,176 @@ __device__ __forceinline__ double take(double acc, float x) {
   }
 }
 
-// The pieces [lo, hi) of this workgroup, one call of f(tensor, first element, end) each.
-template <typename F>
+// The pieces of this workgroup, one call of f(tensor, first element, end)
+// each: [lo, hi) of the tensors laid end to end, from the first to the last, or
+// from the last to the first.
+template <bool BACK, typename F>
 __device__ __forceinline__ void for_pieces(const GradTable& t, F f) {
   const int64_t total = t.piece_end[t.count - 1];
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-  int i = 0;
-  for (int64_t p = lo; p < hi; ++p) {
-    while (p >= t.piece_end[i]) ++i;
-    const int64_t per = kPiece / (t.dtype[i] == LBQ_F32 ? 4 : 2);
-    const int64_t first = (p - (i == 0 ? 0 : t.piece_end[i - 1])) * per;
-    f(i, first, min(first + per, (int64_t)t.numel[i]));
+  const int lo = (int)(total * blockIdx.x / gridDim.x), hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  if (lo >= hi) return;
+  // the tensor of the piece to start with: the first whose end lies behind it
+  int a = 0, b = t.count - 1;
+  while (a < b) {
+    const int mid = (a + b) >> 1;
+    if (t.piece_end[mid] > (BACK ? hi - 1 : lo)) b = mid;
+    else a = mid + 1;
   }
+  int begin = a == 0 ? 0 : t.piece_end[a - 1], end = t.piece_end[a];
+  for (int n = 0; n < hi - lo; ++n) {
+    const int p = BACK ? hi - 1 - n : lo + n;
+    if constexpr (BACK) {
+      while (p < begin) end = begin, --a, begin = a == 0 ? 0 : t.piece_end[a - 1];
+    } else {
+      while (p >= end) begin = end, ++a, end = t.piece_end[a];
+    }
+    const int64_t per = kPiece / (t.dtype[a] == LBQ_F32 ? 4 : 2);
+    const int64_t first = (int64_t)(p - begin) * per;
+    f(a, first, min(first + per, t.numel[a]));
+  }
+}
+
+constexpr int kLoads = kPiece / (kThreads * 16);  // 16-byte loads of a thread and piece
+
+__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Value i of a 16-byte chunk.
+template <int DT>
+__device__ __forceinline__ float value_of(const u32x4_t& v, int i) {
+  if constexpr (DT == LBQ_F32) return __uint_as_float(v[i]);
+  const uint32_t b = (i & 1) ? v[i >> 1] >> 16 : v[i >> 1] & 0xFFFFu;
+  return DT == LBQ_BF16 ? __uint_as_float(b << 16) : f16_bits_to_f32(b);
+}
+
+template <bool INF, int DT>
+__device__ __forceinline__ double take_piece(double acc, const void* g, int64_t first, int64_t end) {
+  constexpr int V = DT == LBQ_F32 ? 4 : 8;  // values of a chunk
+  if (aligned16(g)) {
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(g) + first / V;
+    const int chunks = (int)((end - first) / V);
+    u32x4_t v[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int c = threadIdx.x + kThreads * j;
+      v[j] = c < chunks ? p[c] : u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc = take<INF>(acc, value_of<DT>(v[j], i));
+    first += (int64_t)chunks * V;
+  }
+  for (int64_t e = first + threadIdx.x; e < end; e += kThreads) acc = take<INF>(acc, load_as_f32(g, e, DT));
+  return acc;
 }
 
 template <bool INF>
 __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTable t, double* __restrict__ part) {
   double acc = 0.0;
-  for_pieces(t, [&](int i, int64_t first, int64_t end) {
-    for (int64_t e = first + threadIdx.x; e < end; e += kThreads) acc = take<INF>(acc, load_as_f32(t.grad[i], e, t.dtype[i]));
+  for_pieces<false>(t, [&](int i, int64_t first, int64_t end) {
+    const int dt = t.dtype[i];
+    if (dt == LBQ_F32) acc = take_piece<INF, LBQ_F32>(acc, t.grad[i], first, end);
+    else if (dt == LBQ_BF16) acc = take_piece<INF, LBQ_BF16>(acc, t.grad[i], first, end);
+    else acc = take_piece<INF, LBQ_F16>(acc, t.grad[i], first, end);
   });
-  acc = block_combine<INF>(acc);
+  acc = block_combine<INF, kThreads>(acc);
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
+template <int DT>
+__device__ __forceinline__ uint32_t bits_of(float f) {
+  if constexpr (DT == LBQ_F32) return __float_as_uint(f);
+  return DT == LBQ_BF16 ? bf16_rne_nan(f) : f16_rne(f);
+}
+
+template <int DT>
+__device__ __forceinline__ void scale_piece(const void* g, void* out, float c, int64_t first, int64_t end) {
+  constexpr int V = DT == LBQ_F32 ? 4 : 8;
+  if (aligned16(g) && aligned16(out)) {
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(g) + first / V;
+    u32x4_t* o = reinterpret_cast<u32x4_t*>(out) + first / V;
+    const int chunks = (int)((end - first) / V);
+    u32x4_t v[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int n = threadIdx.x + kThreads * j;
+      if (n < chunks) v[j] = p[n];
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int n = threadIdx.x + kThreads * j;
+      if (n >= chunks) continue;
+      u32x4_t r;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        if constexpr (DT == LBQ_F32) {
+          r[d] = __float_as_uint(value_of<DT>(v[j], d) * c);
+        } else {
+          r[d] = bits_of<DT>(value_of<DT>(v[j], 2 * d) * c) | bits_of<DT>(value_of<DT>(v[j], 2 * d + 1) * c) << 16;
+        }
+      }
+      __builtin_nontemporal_store(r, o + n);
+    }
+    first += (int64_t)chunks * V;
+  }
+  for (int64_t e = first + threadIdx.x; e < end; e += kThreads) {
+    const float v = load_as_f32(g, e, DT) * c;
+    if constexpr (DT == LBQ_F32) static_cast<float*>(out)[e] = v;
+    else static_cast<uint16_t*>(out)[e] = (uint16_t)bits_of<DT>(v);
+  }
+}
+
 // The norm from all the partial values, in every thread.
-template <bool INF>
+template <bool INF, int NT>
 __device__ __forceinline__ float norm_of(const double* __restrict__ part, int parts) {
   double acc = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) {
-    if constexpr (INF) {
-      const uint64_t a = __builtin_bit_cast(uint64_t, acc), b = __builtin_bit_cast(uint64_t, part[i]);
-      acc = __builtin_bit_cast(double, b > a ? b : a);
-    } else {
-      acc += part[i];
+  for (int i = threadIdx.x; i < parts; i += 8 * NT) {  // eight loads in flight
+    double v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j * NT < parts ? part[i + j * NT] : 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (INF) {
+        const uint64_t a = __builtin_bit_cast(uint64_t, acc), b = __builtin_bit_cast(uint64_t, v[j]);
+        acc = __builtin_bit_cast(double, b > a ? b : a);
+      } else {
+        acc += v[j];
+      }
     }
   }
-  acc = block_combine<INF>(acc);
+  acc = block_combine<INF, NT>(acc);
   return (float)(INF ? acc : sqrt(acc));
 }
 
 template <bool INF>
-__global__ __launch_bounds__(kThreads) void k_grad_norm_out(const double* __restrict__ part, int parts,
-                                                           float* __restrict__ norm) {
-  const float n = norm_of<INF>(part, parts);
+__global__ __launch_bounds__(1024) void k_grad_norm_out(const double* __restrict__ part, int parts,
+                                                       float* __restrict__ norm) {
+  const float n = norm_of<INF, 1024>(part, parts);
   if (threadIdx.x == 0) *norm = n;
 }
 
+// Scales the tensors of a table; the norm from `parts` partial values, or from
+// *norm itself (parts == 0) where a launch before this one has summed them.
 template <bool INF>
 __global__ __launch_bounds__(kThreads) void k_grad_scale(GradTable t, const double* __restrict__ part, int parts,
                                                         float max_norm, float* __restrict__ norm) {
-  const float n = norm_of<INF>(part, parts);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  float n;
+  if (parts > 0) {
+    n = norm_of<INF, kThreads>(part, parts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  } else {
+    n = *norm;
+  }
   float c = max_norm / (n + 1e-6f);
   if (c > 1.f) c = 1.f;  // a NaN norm keeps c a NaN
-  for_pieces(t, [&](int i, int64_t first, int64_t end) {
+  for_pieces<true>(t, [&](int i, int64_t first, int64_t end) {
     const int dt = t.dtype[i];
-    if (c == 1.f && t.out[i] == t.grad[i]) return;
-    for (int64_t e = first + threadIdx.x; e < end; e += kThreads) {
-      const float v = load_as_f32(t.grad[i], e, dt) * c;
-      if (dt == LBQ_F32) static_cast<float*>(t.out[i])[e] = v;
-      else static_cast<uint16_t*>(t.out[i])[e] = (uint16_t)(dt == LBQ_BF16 ? bf16_rne_nan(v) : f16_rne(v));
-    }
+    const void* g = t.grad[i];
+    void* out = t.out[i];
+    if (c == 1.f && out == g) return;
+    if (dt == LBQ_F32) scale_piece<LBQ_F32>(g, out, c, first, end);
+    else if (dt == LBQ_BF16) scale_piece<LBQ_BF16>(g, out, c, first, end);
+    else scale_piece<LBQ_F16>(g, out, c, first, end);
   });
 }
 
@@ -165,60 +273,71 @@ bool next_table(const lbq_grad* g, int count, int& at, GradTable& t) {
   return t.count > 0;
 }
 
-// Workgroups of a table with p of all the total pieces: the chip holds eight a CU.
-int groups_of(int64_t p, int64_t total) {
-  if (total <= kGradGroups) return (int)p;
-  const int64_t g = kGradGroups * p / total;
-  return (int)(g < 1 ? 1 : g);
-}
+// Workgroups of a table of p pieces: eight a CU where there are that many.
+int groups_of(int64_t p) { return (int)(p < kGradGroups ? p : kGradGroups); }
 
-}  // namespace
-
-int64_t grad_pieces(const lbq_grad* g, int count) {
-  int64_t total = 0;
-  for (int i = 0; i < count; ++i) total += pieces_of(g[i]);
-  return total;
-}
-
-int grad_parts(const lbq_grad* g, int count) {
-  const int64_t total = grad_pieces(g, count);
+template <bool INF>
+hipError_t norm_launches(const lbq_grad* g, int count, double* part, hipStream_t s) {
   GradTable t;
-  int parts = 0;
-  for (int at = 0; next_table(g, count, at, t);) parts += groups_of(t.piece_end[t.count - 1], total);
-  return parts;
-}
-
-hipError_t launch_grad_norm(const lbq_grad* g, int count, bool inf, double* part, hipStream_t s) {
-  const int64_t total = grad_pieces(g, count);
-  GradTable t;
-  int parts = 0;
   for (int at = 0; next_table(g, count, at, t);) {
-    const int groups = groups_of(t.piece_end[t.count - 1], total);
-    if (inf) hipLaunchKernelGGL(k_grad_norm<true>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part + parts);
-    else hipLaunchKernelGGL(k_grad_norm<false>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part + parts);
-    parts += groups;
+    const int groups = groups_of(t.piece_end[t.count - 1]);
+    hipLaunchKernelGGL(k_grad_norm<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part);
+    part += groups;
   }
   return hipGetLastError();
 }
 
+template <bool INF>
+hipError_t scale_launches(const lbq_grad* g, int count, const double* part, int parts, float max_norm, float* norm,
+                          hipStream_t s) {
+  // One table: its workgroups sum the partial values themselves (at most 2048,
+  // from L2).  More: one launch sums them once.
+  if (count > kGradTable) {
+    hipLaunchKernelGGL(k_grad_norm_out<INF>, dim3(1), dim3(1024), 0, s, part, parts, norm);
+    parts = 0;
+  }
+  // The last table first, and each from its end (for_pieces): what the sums
+  // read last is still in the Infinity Cache.
+  int full = 0;
+  for (int i = 0; i < count; ++i) full += g[i].numel > 0;
+  for (int first = full > 0 ? (full - 1) / kGradTable * kGradTable : -1; first >= 0; first -= kGradTable) {
+    GradTable t;
+    int at = 0;
+    for (int skip = first; skip > 0 || g[at].numel == 0; ++at) skip -= g[at].numel > 0;
+    next_table(g, count, at, t);
+    const int groups = groups_of(t.piece_end[t.count - 1]);
+    hipLaunchKernelGGL(k_grad_scale<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part, parts, max_norm, norm);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int grad_parts(const lbq_grad* g, int count) {
+  int parts = 0;
+  int64_t pieces = 0;
+  for (int i = 0, n = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    pieces += pieces_of(g[i]);
+    if (++n % kGradTable == 0) parts += groups_of(pieces), pieces = 0;
+  }
+  return parts + groups_of(pieces);
+}
+
+hipError_t launch_grad_norm(const lbq_grad* g, int count, bool inf, double* part, hipStream_t s) {
+  return inf ? norm_launches<true>(g, count, part, s) : norm_launches<false>(g, count, part, s);
+}
+
 hipError_t launch_grad_norm_out(bool inf, const double* part, int parts, float* norm, hipStream_t s) {
-  if (inf) hipLaunchKernelGGL(k_grad_norm_out<true>, dim3(1), dim3(kThreads), 0, s, part, parts, norm);
-  else hipLaunchKernelGGL(k_grad_norm_out<false>, dim3(1), dim3(kThreads), 0, s, part, parts, norm);
+  if (inf) hipLaunchKernelGGL(k_grad_norm_out<true>, dim3(1), dim3(1024), 0, s, part, parts, norm);
+  else hipLaunchKernelGGL(k_grad_norm_out<false>, dim3(1), dim3(1024), 0, s, part, parts, norm);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_scale(const lbq_grad* g, int count, bool inf, const double* part, int parts, float max_norm,
                              float* norm, hipStream_t s) {
-  const int64_t total = grad_pieces(g, count);
-  GradTable t;
-  bool first = true;
-  for (int at = 0; next_table(g, count, at, t); first = false) {
-    const int groups = groups_of(t.piece_end[t.count - 1], total);
-    float* out = first ? norm : nullptr;
-    if (inf) hipLaunchKernelGGL(k_grad_scale<true>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part, parts, max_norm, out);
-    else hipLaunchKernelGGL(k_grad_scale<false>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part, parts, max_norm, out);
-  }
-  return hipGetLastError();
+  return inf ? scale_launches<true>(g, count, part, parts, max_norm, norm, s)
+             : scale_launches<false>(g, count, part, parts, max_norm, norm, s);
 }
 
 }  // namespace lbq

@@ -209,8 +209,7 @@ struct GradTable {
   uint8_t dtype[kGradTable];
   int count;
 };
-constexpr int kGradGroups = 2048;  // workgroups over all the launches of one pass (a few more when there are many)
-int64_t grad_pieces(const lbq_grad* g, int count);
+constexpr int kGradGroups = 2048;  // most workgroups of a launch, each with a partial value
 int grad_parts(const lbq_grad* g, int count);
 hipError_t launch_grad_norm(const lbq_grad* g, int count, bool inf, double* part, hipStream_t s);
 hipError_t launch_grad_norm_out(bool inf, const double* part, int parts, float* norm, hipStream_t s);

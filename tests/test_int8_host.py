@@ -249,9 +249,9 @@ def test_norm_refusals_and_workspace(L):
     assert status(L, L.lib.lbq_grad_norm(2, t, 5, A, A, 1 << 20, None)) == "LBQ_E_FORMAT"
     assert status(L, L.lib.lbq_grad_norm(2, t, 0, None, A, 1 << 20, None)) == "LBQ_E_NULL"
     assert status(L, L.lib.lbq_grad_norm(2, t, 0, A, None, 0, None)) == "LBQ_E_WORKSPACE"
-    # the workspace does not grow with the gradients: one partial sum a workgroup
+    # the workspace does not grow with the gradients: one partial sum a workgroup, and a launch takes 120 tensors
     big = grads_of(L, *[(A, A, 1 << 30, 0)] * 300)
-    assert 0 < L.lib.lbq_grad_workspace_bytes(300, big) <= 8 * (2048 + 16)
+    assert 0 < L.lib.lbq_grad_workspace_bytes(300, big) <= 3 * 8 * 2048
     assert L.lib.lbq_grad_workspace_bytes(1, grads_of(L, (None, None, 0, 0))) == 0
 
 
