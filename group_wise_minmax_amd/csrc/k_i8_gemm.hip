@@ -7,17 +7,13 @@
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"
+#include <algorithm>
+#include <cstdlib>
+#include <cstdio>
 
 namespace lbq {
 
 namespace {
-
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ i32x4_t mfma_i8(const i32x4_t& a, const i32x4_t& b, const i32x4_t& c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-}
-
 
 // 16 bytes a lane from r (byte offset voff of the lane plus soff) to LDS: lane
 // l's at `lds` + 16 l, `lds` the same in the whole wave.  (The host pass knows
@@ -28,7 +24,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int8_t* ld
 #endif
 }
 
-// One K step of a tile in LDS: BN rows of W and BM rows of X, 64 bytes each.
+// 64 codes of K of a tile in LDS: BN rows of W and BM rows of X, 64 bytes each.
 // Chunk c (16 bytes) of row r lies at position c ^ key(r): the 16 lanes that a
 // 16-byte LDS read serves together (0-3, 12-15, 20-23 and 24-27 of a half wave,
 // or the other 16) then read 16 different sixteenths of the 64 banks, where
@@ -40,8 +36,7 @@ struct I8Stage {
 };
 __device__ __forceinline__ int i8_key(int r) { return -(r >> 2) & 3; }
 
-constexpr int I8K = 64;      // K step
-constexpr int kStages = 4;   // stages in LDS
+constexpr int I8K = 64;
 
 // Order of a half step's instructions: R LDS reads and L loads, one after each
 // MFMA, then the rest of the M MFMAs.
@@ -61,27 +56,35 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+constexpr int kGemmThreads = 512;
+constexpr int kGemmLds = 1 << 17;
+constexpr int kStages = 4;
+// A K step of a tile, one stage in LDS, is KS slices of 64 codes: the barrier
+// of a step costs some 300 cycles, so a step holds at least 512 cycles of a
+// SIMD's MFMAs (128 x 128 tiles: 2 slices, k = 4096 22 -> 1x us).
+template <int BN, int BM>
+constexpr int i8_slices() {
+  return kStages * 2 * (int)sizeof(I8Stage<BN, BM>) <= kGemmLds ? 2 : 1;
+}
+
+// The BN x BM outputs from channel n0 of weight wi and token m0 on, by WGN x
+// WGM waves, summed over `slices` slices of K from s0 on.  With `part` the integer
+// sums go there, [m][n], instead of the outputs to Y.
 template <int BN, int BM, int WGN, int WGM, bool LORA>
-__global__ __launch_bounds__(64 * WGN * WGM, 1) void k_i8_gemm(I8Set set, const int8_t* __restrict__ Xq,
-                                                              const float* __restrict__ xs, int m, int k, LoraEpi lora) {
+__device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restrict__ Xq, const float* __restrict__ xs,
+                                        int m, int k, const LoraEpi& lora, int wi, int n0, int m0, int s0, int slices,
+                                        int* __restrict__ part, int8_t* lds) {
   constexpr int NW = WGN * WGM;
   constexpr int TN = BN / WGN / 16, TM = BM / WGM / 16, TH = TN / 2;
   constexpr int LW = BN / 16 / NW, LX = BM / 16 / NW;  // 1-KiB pieces (16 rows) a wave loads of each operand
-  static_assert(LW * NW * 16 == BN && LX * NW * 16 == BM, "whole pieces");
-  __shared__ __attribute__((aligned(16))) I8Stage<BN, BM> st[kStages];
+  static_assert(NW * 64 == kGemmThreads && LW * NW * 16 == BN && LX * NW * 16 == BM, "whole pieces");
+  constexpr int S = kStages, KS = i8_slices<BN, BM>();
+  auto& st = *reinterpret_cast<I8Stage<BN, BM>(*)[S][KS]>(lds);
+  static_assert(sizeof(st) <= kGemmLds, "stages fit");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wn = wave % WGN, wm = wave / WGN;
-  const int nx = set.tile_end[set.count - 1], ny = (m + BM - 1) / BM;
-  int tx, ty;
-  tile_of(blockIdx.x, nx, ny, tx, ty);
-  int wi = 0;
-#pragma unroll
-  for (int i = 1; i < kGemvMaxGroup; ++i)
-    if (i < set.count && tx >= set.tile_end[i - 1]) wi = i;
-  if (wi > 0) tx -= set.tile_end[wi - 1];
   const int n = set.n[wi];
-  const int n0 = tx * BN, m0 = ty * BM;
 
   // Global loads go straight to LDS: a wave's load fills 16 rows, lane l the
   // 16 bytes at position l % 4 of row l / 4, which hold chunk (l % 4) ^ key(row).
@@ -94,13 +97,20 @@ __global__ __launch_bounds__(64 * WGN * WGM, 1) void k_i8_gemm(I8Set set, const 
   for (int i = 0; i < LW; ++i) ow[i] = min(n0 + 16 * (wave * LW + i) + lr, n - 1) * k + lc;
 #pragma unroll
   for (int i = 0; i < LX; ++i) ox[i] = min(m0 + 16 * (wave * LX + i) + lr, m - 1) * k + lc;
-  auto load_w = [&](int8_t* w, int kt) {
+  // The loads of step t; slices past the last one repeat it (they are not
+  // multiplied), so that the count of loads in flight stays what the wait says.
+  auto at = [&](int t, int c) { return I8K * (s0 + min(KS * t + c, slices - 1)); };
+  auto load_w = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < LW; ++i) load_to_lds(rw, w + 1024 * (wave * LW + i), ow[i], kt);
+    for (int c = 0; c < KS; ++c)
+#pragma unroll
+      for (int i = 0; i < LW; ++i) load_to_lds(rw, st[t % S][c].w + 1024 * (wave * LW + i), ow[i], at(t, c));
   };
-  auto load_x = [&](int8_t* x, int kt) {
+  auto load_x = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < LX; ++i) load_to_lds(rx, x + 1024 * (wave * LX + i), ox[i], kt);
+    for (int c = 0; c < KS; ++c)
+#pragma unroll
+      for (int i = 0; i < LX; ++i) load_to_lds(rx, st[t % S][c].x + 1024 * (wave * LX + i), ox[i], at(t, c));
   };
 
   i32x4_t acc[TN][TM];
@@ -130,54 +140,88 @@ __global__ __launch_bounds__(64 * WGN * WGM, 1) void k_i8_gemm(I8Set set, const 
       for (int b = 0; b < TM; ++b) acc[half * TH + a][b] = mfma_i8(w[a], x[b], acc[half * TH + a][b]);
   };
 
-  // Step t lies in stage t % 4.  While it is multiplied, steps t + 1 and t + 2
-  // are on their way and the loads of step t + 3 are issued, spread between
+  // Step t lies in stage t % S.  While it is multiplied, steps t + 1 to t + S - 2
+  // are on their way and the loads of step t + S - 1 are issued, spread between
   // the MFMAs (issued together they fill the load queue and hold up the wave's
-  // MFMAs behind them).  The first slice of a step is read before the last
-  // MFMAs of the one before it.  Past the last step the loads repeat it, so
-  // that the count of loads in flight stays what the wait says.
-  const int steps = k / I8K;
-  auto at = [&](int t) { return I8K * min(t, steps - 1); };
-  // Steps up to t + 1 are there: this wave's loads but the last two steps'
-  // (vmcnt), and by the barrier every wave's; every wave has read step t.
+  // MFMAs behind them).  The first operands of a step are read before the last
+  // MFMAs of the one before it.
+  //
+  // In step t: step t + 1 is there, by this wave's loads (all but those of the
+  // steps after it: vmcnt) and by the barrier every wave's; and every wave has
+  // read step t.
+  constexpr int kLater = KS * ((S - 3) * (LW + LX) + LW);
+  static_assert(kLater < 16, "vmcnt's low four bits");
   auto arrive = [&]() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (LW + LW + LX));  // lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(0x0070 | kLater);  // lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  for (int t = 0; t < 3; ++t) {
-    load_w(st[t].w, at(t));
-    load_x(st[t].x, at(t));
+  const int steps = slices / KS;
+#pragma unroll
+  for (int t = 0; t < S - 1; ++t) {
+    load_w(t);
+    load_x(t);
   }
   arrive();
-  read_w(st[0], 0, w0);
-  read_x(st[0], x0);
-  // xa: this step's tokens, xb: the next one's
-  auto step = [&](int t, const i32x4_t (&xa)[TM], i32x4_t (&xb)[TM]) {
-    I8Stage<BN, BM>& cur = st[t % kStages];
-    I8Stage<BN, BM>& next = st[(t + 1) % kStages];
-    I8Stage<BN, BM>& far = st[(t + 3) % kStages];
-    read_w(cur, 1, w1);
-    load_w(far.w, at(t + 3));
-    mma(0, w0, xa);
-    interleave<TH, LW, TH * TM>();
-    arrive();
-    read_w(next, 0, w0);
-    read_x(next, xb);
-    load_x(far.x, at(t + 3));
-    mma(1, w1, xa);
-    interleave<TH + TM, LX, TH * TM>();
+  read_w(st[0][0], 0, w0);
+  read_x(st[0][0], x0);
+  // xa: the tokens of this step's first slice, xb: those of the next slice
+  auto step = [&](int t, i32x4_t (&xa)[TM], i32x4_t (&xb)[TM]) {
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      const I8Stage<BN, BM>& cur = st[t % S][c];
+      const I8Stage<BN, BM>& next = c + 1 < KS ? st[t % S][c + 1] : st[(t + 1) % S][0];
+      i32x4_t(&x)[TM] = (c & 1) ? xb : xa;
+      i32x4_t(&y)[TM] = (c & 1) ? xa : xb;
+      read_w(cur, 1, w1);
+      if (c == 0) load_w(t + S - 1);
+      mma(0, w0, x);
+      interleave<TH, (KS == 1 ? LW : 0), TH * TM>();
+      if (c + 1 == KS) arrive();
+      read_w(next, 0, w0);
+      read_x(next, y);
+      if (c + 1 == KS) load_x(t + S - 1);
+      mma(1, w1, x);
+      interleave<TH + TM, (KS == 1 ? LX : 0), TH * TM>();
+    }
   };
   int t = 0;
   for (; t + 1 < steps; t += 2) {
     step(t, x0, x1);
-    step(t + 1, x1, x0);
+    if constexpr (KS == 1) step(t + 1, x1, x0);
+    else step(t + 1, x0, x1);
   }
   if (t < steps) step(t, x0, x1);
+  if (KS == 2 && slices % 2 != 0) {  // half a step
+    read_w(st[steps % S][0], 1, w1);
+    mma(0, w0, x0);
+    mma(1, w1, x0);
+  }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // no load to LDS is left behind
 
   // Epilogue: lane l holds channels n = 4 (l / 16) + i of token m = l % 16.
+  if (part != nullptr) {
+    const bool vec = (n & 3) == 0;
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+      const int mr = m0 + (wm * TM + b) * 16 + li;
+      if (mr >= m) continue;
+      int* prow = part + (int64_t)mr * n;
+#pragma unroll
+      for (int a = 0; a < TN; ++a) {
+        const int nb = n0 + (wn * TN + a) * 16 + 4 * lg;
+        if (vec && nb < n) {
+          *reinterpret_cast<i32x4_t*>(prow + nb) = acc[a][b];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (nb + i < n) prow[nb + i] = acc[a][b][i];
+        }
+      }
+    }
+    return;
+  }
   const __amdgpu_buffer_rsrc_t rsw = make_rsrc(set.ws[wi], (int64_t)n * 4);
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(xs, (int64_t)m * 4);
   f32x4_t out[TN][TM];
@@ -250,32 +294,112 @@ __global__ __launch_bounds__(64 * WGN * WGM, 1) void k_i8_gemm(I8Set set, const 
   }
 }
 
-template <int BN, int BM, int WGN, int WGM>
-hipError_t launch_gemm(I8Set set, const int8_t* Xq, const float* xs, int64_t m, int64_t k, const LoraEpi& lora,
-                       hipStream_t s) {
-  int end = 0;
-  for (int i = 0; i < set.count; ++i) {
-    end += (set.n[i] + BN - 1) / BN;
-    set.tile_end[i] = end;
+// Tiles of one launch: 256 x 256 outputs each, numbered over all the weights'
+// row tiles; the first `whole` of them by one workgroup each, the others cut
+// into `cut` pieces (2: 128 x 256, 4: 128 x 128).  With ks > 1 (only where
+// nothing is whole) K is split into ks ranges of `per` steps, gridDim.y of them,
+// whose integer sums k_i8_reduce adds.
+struct I8Plan {
+  int nx, ny;
+  int whole, cut;
+  int ks, per;
+};
+
+template <bool LORA>
+__global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan plan, const int8_t* __restrict__ Xq,
+                                                            const float* __restrict__ xs, int m, int k, LoraEpi lora,
+                                                            int* __restrict__ part) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kGemmLds];
+  const int bid = blockIdx.x;
+  const bool whole = bid < plan.whole;
+  const int t = whole ? xcd_order(bid, plan.whole) : xcd_order(bid - plan.whole, gridDim.x - plan.whole);
+  const int piece = whole ? 0 : t % plan.cut;
+  int tx, ty;
+  tile_at(whole ? t : plan.whole + t / plan.cut, plan.nx, plan.ny, tx, ty);
+  int wi = 0;
+#pragma unroll
+  for (int i = 1; i < kGemvMaxGroup; ++i)
+    if (i < set.count && tx >= set.tile_end[i - 1]) wi = i;
+  if (wi > 0) tx -= set.tile_end[wi - 1];
+  const int n0 = tx * 256 + 128 * (piece & 1), m0 = ty * 256 + 128 * (piece >> 1);
+  if (n0 >= set.n[wi] || m0 >= m) return;
+  const int s0 = blockIdx.y * plan.per, steps = min(k / I8K - s0, plan.per);
+  if (part != nullptr) part += (int64_t)m * ((int64_t)blockIdx.y * set.n_end[set.count - 1] + (wi == 0 ? 0 : set.n_end[wi - 1]));
+  if (whole) i8_tile<256, 256, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
+  else if (plan.cut == 2) i8_tile<128, 256, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
+  else i8_tile<128, 128, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, s0, steps, part, lds);
+}
+
+// Outputs from the integer sums of ks K ranges: one thread for four channels of
+// a token.
+__global__ __launch_bounds__(256) void k_i8_reduce(I8Set set, const int* __restrict__ part, int ks,
+                                                  const float* __restrict__ xs, int m, LoraEpi lora) {
+  const int wi = blockIdx.z;
+  const int n = set.n[wi];
+  const int nb = 4 * (blockIdx.x * 256 + threadIdx.x), mr = blockIdx.y;
+  if (nb >= n) return;
+  const int64_t stride = (int64_t)m * set.n_end[set.count - 1];
+  const int* p = part + (int64_t)m * (wi == 0 ? 0 : set.n_end[wi - 1]) + (int64_t)mr * n + nb;
+  int acc[4] = {0, 0, 0, 0};
+  if ((n & 3) == 0) {
+    i32x4_t v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int j = 0; j < ks; ++j) v += *reinterpret_cast<const i32x4_t*>(p + j * stride);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = v[i];
+  } else {
+    for (int j = 0; j < ks; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (nb + i < n) acc[i] += p[j * stride + i];
   }
-  const dim3 grid((unsigned)(end * ((m + BM - 1) / BM)));
-  if (lora.t != nullptr)
-    hipLaunchKernelGGL((k_i8_gemm<BN, BM, WGN, WGM, true>), grid, dim3(64 * WGN * WGM), 0, s, set, Xq, xs, (int)m, (int)k, lora);
-  else
-    hipLaunchKernelGGL((k_i8_gemm<BN, BM, WGN, WGM, false>), grid, dim3(64 * WGN * WGM), 0, s, set, Xq, xs, (int)m, (int)k, lora);
-  return hipGetLastError();
+  i8_store(set, wi, xs[mr], acc, mr, nb, lora);
+}
+
+// Whole rounds of 256 x 256 tiles (one a CU); a last round that would leave
+// half of the chip idle is cut into 128 x 256 pieces, one that would leave three
+// quarters idle into 128 x 128 pieces.
+I8Plan plan_of(const int* tile_end, int count, int64_t k, int64_t m) {
+  I8Plan p;
+  p.nx = tile_end[count - 1];
+  p.ny = (int)((m + 255) / 256);
+  const int tiles = p.nx * p.ny, rest = tiles % 256, steps = (int)(k / I8K);
+  p.whole = rest <= 128 ? tiles - rest : tiles;
+  p.cut = rest <= 64 ? 4 : 2;
+  p.ks = 1;
+  p.per = steps;
+  if (const char* e = getenv("I8KS")) {
+    int ks = atoi(e);
+    if (ks > 1 && p.whole == 0 && p.cut == 4) {
+      p.per = (steps + ks - 1) / ks;
+      p.ks = (steps + p.per - 1) / p.per;
+    }
+  }
+  return p;
 }
 
 }  // namespace
 
-size_t i8_fwd_workspace_bytes(const int64_t*, int, int64_t, int64_t) { return 0; }
+size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
+  int tile_end[kGemvMaxGroup];
+  int end = 0;
+  int64_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    end += (int)((ns[i] + 255) / 256);
+    tile_end[i] = end;
+    n += ns[i];
+  }
+  const I8Plan plan = plan_of(tile_end, count, k, m);
+  return plan.ks > 1 ? (size_t)plan.ks * (size_t)m * (size_t)n * sizeof(int) : 0;
+}
 
 hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows,
-                         int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void*,
+                         int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void* work,
                          hipStream_t s) {
   I8Set set{};
   set.count = count;
-  int64_t t256 = 0;
+  int end = 0, most = 0;
+  int64_t n = 0;
   for (int i = 0; i < count; ++i) {
     set.w[i] = reinterpret_cast<const int8_t*>(ws[i].packed);
     set.ws[i] = ws[i].scales;
@@ -283,11 +407,28 @@ hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ld
     set.rows[i] = out_rows[i];
     set.ldy[i] = ldys[i];
     set.n[i] = (int)ws[i].n;
-    t256 += (ws[i].n + 255) / 256 * ((m + 255) / 256);
+    end += (int)((ws[i].n + 255) / 256);
+    set.tile_end[i] = end;
+    n += ws[i].n;
+    set.n_end[i] = n;
+    most = std::max(most, set.n[i]);
   }
-  const int64_t k = ws[0].k;
-  if (t256 >= 128) return launch_gemm<256, 256, 2, 4>(set, Xq, xs, m, k, lora, s);
-  return launch_gemm<128, 128, 2, 2>(set, Xq, xs, m, k, lora, s);
+  if (const char* e = getenv("I8SK")) {
+    int tn, tm;
+    if (sscanf(e, "%d,%d", &tn, &tm) == 2 && tn > 0) return launch_i8_skinny(set, tn, tm, Xq, xs, m, ws[0].k, lora, s);
+  }
+  const int k = (int)ws[0].k;
+  const I8Plan plan = plan_of(set.tile_end, count, k, m);
+  int* part = plan.ks > 1 ? static_cast<int*>(work) : nullptr;
+  const dim3 grid((unsigned)(plan.whole + (plan.nx * plan.ny - plan.whole) * plan.cut), (unsigned)plan.ks);
+  if (lora.t != nullptr && plan.ks == 1)
+    hipLaunchKernelGGL(k_i8_gemm<true>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, k, lora, part);
+  else
+    hipLaunchKernelGGL(k_i8_gemm<false>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, k, lora, part);
+  if (part != nullptr)
+    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)((most + 1023) / 1024), (unsigned)m, (unsigned)count), dim3(256), 0, s,
+                       set, part, plan.ks, xs, (int)m, lora);
+  return hipGetLastError();
 }
 
 }  // namespace lbq

@@ -57,6 +57,14 @@ __device__ __forceinline__ f32x4_t mfma16x16x32(const u32x4_t& a, const u32x4_t&
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// D(16x16, i32) += A(16x64) * B(64x16), 8-bit operands in the same lane order:
+// lane l holds 16 bytes of row (column) l%16, D[4*(l/16) + i][l%16].
+__device__ __forceinline__ i32x4_t mfma_i8(const i32x4_t& a, const i32x4_t& b, const i32x4_t& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
 // Sum over the 64 lanes of a wave, result in every lane: four DPP steps
 // (xor 1, xor 2 within quads, half-row and row mirrors) and two cross-row
 // exchanges.
@@ -106,16 +114,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, int64
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes, 0x00020000);
 }
 
-// Tile index of workgroup `bid` among nx * ny tiles, XCD-aware and grouped.
-__device__ __forceinline__ void tile_of(int bid, int nx, int ny, int& tx, int& ty) {
-  const int total = nx * ny;
-  // hardware round-robins workgroups over 8 XCDs: give XCD j the contiguous
-  // logical range [j*per, (j+1)*per) (the remainder goes to the first XCDs)
+// Position of workgroup `bid` among `total` in an XCD-aware order: hardware
+// round-robins workgroups over 8 XCDs; XCD j gets the contiguous range
+// [j*per, (j+1)*per) (the remainder goes to the first XCDs).
+__device__ __forceinline__ int xcd_order(int bid, int total) {
   const int xcd = bid & 7, slot = bid >> 3;
   const int per = total >> 3, rem = total & 7;
   const int start = xcd * per + (xcd < rem ? xcd : rem);
   int t = start + slot;
   if (slot >= per + (xcd < rem ? 1 : 0)) t = bid;  // cannot happen for grid == total
+  return t;
+}
+
+// Tile t of nx * ny, walked in groups of X-row tiles.
+__device__ __forceinline__ void tile_at(int t, int nx, int ny, int& tx, int& ty) {
   constexpr int GM = 4;  // X-row tiles per group (measured: 2 -> 4 +1.5% on the 8B layer at m = 4096)
   const int group = t / (GM * nx);
   const int first = group * GM;
@@ -123,6 +135,11 @@ __device__ __forceinline__ void tile_of(int bid, int nx, int ny, int& tx, int& t
   const int r = t - group * GM * nx;
   ty = first + r % gm;
   tx = r / gm;
+}
+
+// Tile index of workgroup `bid` among nx * ny tiles, XCD-aware and grouped.
+__device__ __forceinline__ void tile_of(int bid, int nx, int ny, int& tx, int& ty) {
+  tile_at(xcd_order(bid, nx * ny), nx, ny, tx, ty);
 }
 
 // compact: fp16 scales and zero points packed `bits` wide, like the codes.
@@ -302,6 +319,42 @@ __device__ __forceinline__ float nf4_block_scale(const WView& w, int64_t blk, fl
 
 // bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
 __device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
+
+// Outputs of channels nb .. nb + 3 (nb < n) of weight wi and token mr from their
+// integer sums: scaled (one rounding to fp32 each: the caller's file has
+// contraction off), the adapter term T[mr] . B[channel] added in fp32.
+__device__ __forceinline__ void i8_store(const I8Set& set, int wi, float sx, const int acc[4], int64_t mr, int nb,
+                                         const LoraEpi& lora) {
+#pragma clang fp contract(off)
+  const int n = set.n[wi];
+  const float* sw = set.ws[wi];
+  const int32_t* rows = set.rows[wi];
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * sx * sw[nb + i < n ? nb + i : n - 1];
+  if (lora.t != nullptr) {
+    const uint16_t* t = lora.t + mr * lora.rp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t* b = lora.b + (int64_t)(nb + i < n ? nb + i : n - 1) * lora.r;
+      float d = 0.f;
+      for (int q = 0; q < lora.r; ++q)
+        d = fmaf(__uint_as_float((uint32_t)t[q] << 16), __uint_as_float((uint32_t)b[q] << 16), d);
+      v[i] += d;
+    }
+  }
+  uint16_t* y = set.y[wi] + mr * set.ldy[wi];
+  uint2 o;
+  o.x = cvt_pk_bf16(v[0], v[1]);
+  o.y = cvt_pk_bf16(v[2], v[3]);
+  if (rows == nullptr && nb + 3 < n && (reinterpret_cast<uintptr_t>(y + nb) & 7) == 0) {
+    *reinterpret_cast<uint2*>(y + nb) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (nb + i < n) y[rows != nullptr ? rows[nb + i] : nb + i] = (uint16_t)((i < 2 ? o.x : o.y) >> (16 * (i & 1)));
+  }
+}
 
 // Dispatch a functor templated on the weight kind (the group-wise formats and
 // NF4; 8-bit rows have kernels of their own and an input-gradient variant).

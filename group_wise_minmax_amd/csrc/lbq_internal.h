@@ -188,6 +188,7 @@ struct I8Set {
   int64_t ldy[kGemvMaxGroup];
   int n[kGemvMaxGroup];
   int tile_end[kGemvMaxGroup];  // weight i owns the row tiles [tile_end[i-1], tile_end[i])
+  int64_t n_end[kGemvMaxGroup];  // channels of weights 0 .. i
   int count;
 };
 // The product on quantized tokens Xq [m][k] with scales xs [m], for up to
@@ -197,6 +198,11 @@ size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m
 hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows,
                          int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void* work,
                          hipStream_t s);
+
+// The same by workgroups of 16 tn channels and 16 tm tokens (tn, tm in {1, 2, 4})
+// that split K over their waves; set.tile_end is not looked at.
+hipError_t launch_i8_skinny(const I8Set& set, int tn, int tm, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
+                            const LoraEpi& lora, hipStream_t s);
 
 // ---- gradient norm (k_grad.hip) -------------------------------------------------
 // Tensors of one launch, in the kernel's arguments (they may take 4 KiB).
