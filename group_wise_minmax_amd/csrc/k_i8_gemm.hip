@@ -57,7 +57,8 @@ __device__ __forceinline__ void interleave() {
 }
 
 constexpr int kGemmThreads = 512;
-constexpr int kGemmLds = 1 << 17;
+constexpr int kGemmLds = 1 << 17;  // bytes of LDS for the stages
+constexpr int kGemmOut = 1 << 15;  // and for the outputs on their way to memory
 constexpr int kStages = 4;
 // A K step of a tile, one stage in LDS, is KS slices of 64 codes: the barrier
 // of a step costs some 300 cycles, so a step holds at least 512 cycles of a
@@ -270,27 +271,50 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   uint16_t* Y = set.y[wi];
   const int32_t* rows = set.rows[wi];
   const int64_t ldy = set.ldy[wi];
-  const bool vec = rows == nullptr && (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(Y) & 7) == 0;
+  // A lane's values lie in one token each, four channels of it: stored from here
+  // they are 32-byte runs.  Through LDS (16 tokens at a time, in the wave's own
+  // part) a token's TN * 16 channels of the wave follow one another, 16 bytes a
+  // lane.  Chunk c of token r lies at position c ^ (r & (TN * 2 - 1)).
+  if (rows == nullptr && (ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(Y) & 15) == 0 &&
+      n0 + (wn + 1) * TN * 16 <= n) {
+    constexpr int C = TN * 2, R = 64 / C;  // 16-byte chunks of a token, tokens of a store
+    int8_t* buf = lds + kGemmLds + wave * (16 * C * 16);
+    uint16_t* yw = Y + n0 + wn * TN * 16;
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+#pragma unroll
+      for (int a = 0; a < TN; ++a) {
+        uint2 o;
+        o.x = cvt_pk_bf16(out[a][b][0], out[a][b][1]);
+        o.y = cvt_pk_bf16(out[a][b][2], out[a][b][3]);
+        *reinterpret_cast<uint2*>(buf + li * C * 16 + 16 * ((2 * a + (lg >> 1)) ^ (li & (C - 1))) + 8 * (lg & 1)) = o;
+      }
+      u32x4_t v[16 / R];
+#pragma unroll
+      for (int i = 0; i < 16 / R; ++i) {
+        const int r = i * R + lane / C, c = lane % C;
+        v[i] = *reinterpret_cast<const u32x4_t*>(buf + r * C * 16 + 16 * (c ^ (r & (C - 1))));
+      }
+#pragma unroll
+      for (int i = 0; i < 16 / R; ++i) {
+        const int mr = m0 + (wm * TM + b) * 16 + i * R + lane / C;
+        if (mr < m) *reinterpret_cast<u32x4_t*>(yw + (int64_t)mr * ldy + 8 * (lane % C)) = v[i];
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int b = 0; b < TM; ++b) {
     const int mr = m0 + (wm * TM + b) * 16 + li;
     if (mr >= m) continue;
     uint16_t* yrow = Y + (int64_t)mr * ldy;
 #pragma unroll
-    for (int a = 0; a < TN; ++a) {
-      const int nb = n0 + (wn * TN + a) * 16 + 4 * lg;
-      uint2 o;
-      o.x = cvt_pk_bf16(out[a][b][0], out[a][b][1]);
-      o.y = cvt_pk_bf16(out[a][b][2], out[a][b][3]);
-      if (vec && nb + 3 < n) {
-        *reinterpret_cast<uint2*>(yrow + nb) = o;
-      } else {
+    for (int a = 0; a < TN; ++a)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (nb + i < n)
-            yrow[rows != nullptr ? rows[nb + i] : nb + i] = (uint16_t)((i < 2 ? o.x : o.y) >> (16 * (i & 1)));
+      for (int i = 0; i < 4; ++i) {
+        const int nr = n0 + (wn * TN + a) * 16 + 4 * lg + i;
+        if (nr < n) yrow[rows != nullptr ? rows[nr] : nr] = i8_bf16(out[a][b][i]);
       }
-    }
   }
 }
 
@@ -309,7 +333,7 @@ template <bool LORA>
 __global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan plan, const int8_t* __restrict__ Xq,
                                                             const float* __restrict__ xs, int m, int k, LoraEpi lora,
                                                             int* __restrict__ part) {
-  __shared__ __attribute__((aligned(1024))) int8_t lds[kGemmLds];
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kGemmLds + kGemmOut];
   const int bid = blockIdx.x;
   const bool whole = bid < plan.whole;
   const int t = whole ? xcd_order(bid, plan.whole) : xcd_order(bid - plan.whole, gridDim.x - plan.whole);
