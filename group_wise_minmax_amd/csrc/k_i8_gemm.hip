@@ -69,9 +69,9 @@ constexpr int i8_slices() {
 }
 
 // The BN x BM outputs from channel n0 of weight wi and token m0 on, by WGN x
-// WGM waves, summed over `slices` slices of K from s0 on.  With `part` the integer
-// sums go there, [m][n], instead of the outputs to Y.
-template <int BN, int BM, int WGN, int WGM, bool LORA>
+// WGM waves, summed over `slices` slices of K from s0 on.  With PART the integer
+// sums go to part, [m][n], where that is not null.
+template <int BN, int BM, int WGN, int WGM, bool LORA, bool PART>
 __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restrict__ Xq, const float* __restrict__ xs,
                                         int m, int k, const LoraEpi& lora, int wi, int n0, int m0, int s0, int slices,
                                         int* __restrict__ part, int8_t* lds) {
@@ -202,7 +202,7 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   __builtin_amdgcn_s_waitcnt(0x0F70);  // no load to LDS is left behind
 
   // Epilogue: lane l holds channels n = 4 (l / 16) + i of token m = l % 16.
-  if (part != nullptr) {
+  if (PART && part != nullptr) {
     const bool vec = (n & 3) == 0;
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
@@ -271,50 +271,44 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   uint16_t* Y = set.y[wi];
   const int32_t* rows = set.rows[wi];
   const int64_t ldy = set.ldy[wi];
+  const bool vec = rows == nullptr && (ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(Y) & 15) == 0;
   // A lane's values lie in one token each, four channels of it: stored from here
   // they are 32-byte runs.  Through LDS (16 tokens at a time, in the wave's own
   // part) a token's TN * 16 channels of the wave follow one another, 16 bytes a
   // lane.  Chunk c of token r lies at position c ^ (r & (TN * 2 - 1)).
-  if (rows == nullptr && (ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(Y) & 15) == 0 &&
-      n0 + (wn + 1) * TN * 16 <= n) {
-    constexpr int C = TN * 2, R = 64 / C;  // 16-byte chunks of a token, tokens of a store
-    int8_t* buf = lds + kGemmLds + wave * (16 * C * 16);
-    uint16_t* yw = Y + n0 + wn * TN * 16;
-#pragma unroll
-    for (int b = 0; b < TM; ++b) {
-#pragma unroll
-      for (int a = 0; a < TN; ++a) {
-        uint2 o;
-        o.x = cvt_pk_bf16(out[a][b][0], out[a][b][1]);
-        o.y = cvt_pk_bf16(out[a][b][2], out[a][b][3]);
-        *reinterpret_cast<uint2*>(buf + li * C * 16 + 16 * ((2 * a + (lg >> 1)) ^ (li & (C - 1))) + 8 * (lg & 1)) = o;
-      }
-      u32x4_t v[16 / R];
-#pragma unroll
-      for (int i = 0; i < 16 / R; ++i) {
-        const int r = i * R + lane / C, c = lane % C;
-        v[i] = *reinterpret_cast<const u32x4_t*>(buf + r * C * 16 + 16 * (c ^ (r & (C - 1))));
-      }
-#pragma unroll
-      for (int i = 0; i < 16 / R; ++i) {
-        const int mr = m0 + (wm * TM + b) * 16 + i * R + lane / C;
-        if (mr < m) *reinterpret_cast<u32x4_t*>(yw + (int64_t)mr * ldy + 8 * (lane % C)) = v[i];
-      }
-    }
-    return;
-  }
+  constexpr int C = TN * 2, R = 64 / C;  // 16-byte chunks of a token, tokens of a store
+  int8_t* buf = lds + kGemmLds + wave * (16 * C * 16);
+  const int nb = n0 + wn * TN * 16 + 8 * (lane % C);
 #pragma unroll
   for (int b = 0; b < TM; ++b) {
-    const int mr = m0 + (wm * TM + b) * 16 + li;
-    if (mr >= m) continue;
-    uint16_t* yrow = Y + (int64_t)mr * ldy;
 #pragma unroll
-    for (int a = 0; a < TN; ++a)
+    for (int a = 0; a < TN; ++a) {
+      uint2 o;
+      o.x = cvt_pk_bf16(out[a][b][0], out[a][b][1]);
+      o.y = cvt_pk_bf16(out[a][b][2], out[a][b][3]);
+      *reinterpret_cast<uint2*>(buf + li * C * 16 + 16 * ((2 * a + (lg >> 1)) ^ (li & (C - 1))) + 8 * (lg & 1)) = o;
+    }
+    u32x4_t v[16 / R];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int nr = n0 + (wn * TN + a) * 16 + 4 * lg + i;
-        if (nr < n) yrow[rows != nullptr ? rows[nr] : nr] = i8_bf16(out[a][b][i]);
-      }
+    for (int i = 0; i < 16 / R; ++i) {
+      const int r = i * R + lane / C, c = lane % C;
+      v[i] = *reinterpret_cast<const u32x4_t*>(buf + r * C * 16 + 16 * (c ^ (r & (C - 1))));
+    }
+    const int mr = m0 + (wm * TM + b) * 16 + lane / C;
+    uint16_t* y = Y + (int64_t)mr * ldy;
+    if (vec && nb + 8 <= n) {
+#pragma unroll
+      for (int i = 0; i < 16 / R; ++i)
+        if (mr + i * R < m) *reinterpret_cast<u32x4_t*>(y + (int64_t)i * R * ldy + nb) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16 / R; ++i)
+        if (mr + i * R < m)
+          for (int e = 0; e < 8 && nb + e < n; ++e) {
+            const uint32_t d = e < 4 ? (e < 2 ? v[i][0] : v[i][1]) : (e < 6 ? v[i][2] : v[i][3]);
+            y[(int64_t)i * R * ldy + (rows != nullptr ? rows[nb + e] : nb + e)] = (uint16_t)(d >> (16 * (e & 1)));
+          }
+    }
   }
 }
 
@@ -349,9 +343,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan p
   if (n0 >= set.n[wi] || m0 >= m) return;
   const int s0 = blockIdx.y * plan.per, steps = min(k / I8K - s0, plan.per);
   if (part != nullptr) part += (int64_t)m * ((int64_t)blockIdx.y * set.n_end[set.count - 1] + (wi == 0 ? 0 : set.n_end[wi - 1]));
-  if (whole) i8_tile<256, 256, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
-  else if (plan.cut == 2) i8_tile<128, 256, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
-  else i8_tile<128, 128, 2, 4, LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, s0, steps, part, lds);
+  if (whole) i8_tile<256, 256, 2, 4, LORA, false>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
+  else if (plan.cut == 2) i8_tile<128, 256, 2, 4, LORA, false>(set, Xq, xs, m, k, lora, wi, n0, m0, 0, steps, nullptr, lds);
+  else i8_tile<128, 128, 2, 4, LORA, !LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, s0, steps, part, lds);
 }
 
 // Outputs from the integer sums of ks K ranges: one thread for four channels of
