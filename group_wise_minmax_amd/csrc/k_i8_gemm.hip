@@ -8,33 +8,19 @@
 
 #include "lbq_device.h"
 #include <algorithm>
-#include <cstdlib>
-#include <cstdio>
+#include <cmath>
 
 namespace lbq {
 
 namespace {
 
-// 16 bytes a lane from r (byte offset voff of the lane plus soff) to LDS: lane
-// l's at `lds` + 16 l, `lds` the same in the whole wave.  (The host pass knows
-// no 16-byte form of the builtin.)
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int8_t* lds, int voff, int soff) {
-#ifdef __HIP_DEVICE_COMPILE__
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
-#endif
-}
-
 // 64 codes of K of a tile in LDS: BN rows of W and BM rows of X, 64 bytes each.
-// Chunk c (16 bytes) of row r lies at position c ^ key(r): the 16 lanes that a
-// 16-byte LDS read serves together (0-3, 12-15, 20-23 and 24-27 of a half wave,
-// or the other 16) then read 16 different sixteenths of the 64 banks, where
-// lane l reads chunk l / 16 of row l % 16.
+// chunks in the order of i8_key.
 template <int BN, int BM>
 struct I8Stage {
   int8_t w[BN * 64];
   int8_t x[BM * 64];
 };
-__device__ __forceinline__ int i8_key(int r) { return -(r >> 2) & 3; }
 
 constexpr int I8K = 64;
 
@@ -83,7 +69,8 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   auto& st = *reinterpret_cast<I8Stage<BN, BM>(*)[S][KS]>(lds);
   static_assert(sizeof(st) <= kGemmLds, "stages fit");
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // the same in the wave: scalar load offsets
   const int wn = wave % WGN, wm = wave / WGN;
   const int n = set.n[wi];
 
@@ -374,49 +361,75 @@ __global__ __launch_bounds__(256) void k_i8_reduce(I8Set set, const int* __restr
   i8_store(set, wi, xs[mr], acc, mr, nb, lora);
 }
 
-// Whole rounds of 256 x 256 tiles (one a CU); a last round that would leave
-// half of the chip idle is cut into 128 x 256 pieces, one that would leave three
-// quarters idle into 128 x 128 pieces.
-I8Plan plan_of(const int* tile_end, int count, int64_t k, int64_t m) {
-  I8Plan p;
-  p.nx = tile_end[count - 1];
-  p.ny = (int)((m + 255) / 256);
-  const int tiles = p.nx * p.ny, rest = tiles % 256, steps = (int)(k / I8K);
-  p.whole = rest <= 128 ? tiles - rest : tiles;
-  p.cut = rest <= 64 ? 4 : 2;
-  p.ks = 1;
-  p.per = steps;
-  if (const char* e = getenv("I8KS")) {
-    int ks = atoi(e);
-    if (ks > 1 && p.whole == 0 && p.cut == 4) {
-      p.per = (steps + ks - 1) / ks;
-      p.ks = (steps + p.per - 1) / p.per;
-    }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a product of count weights of ns channels runs: by k_i8_skinny with tiles
+// of 16 * skinny (1, 2, 4), or (0) by k_i8_gemm as `plan` says.
+struct I8Choice {
+  int skinny;
+  I8Plan plan;
+};
+
+// The cheapest by an estimate in microseconds, fitted to the times of all of
+// them on 170 products (m 1 to 3000, n 256 to 20000, k 256 to 28672, weights
+// not in cache): on these the choice is 7% off the best one on average.
+//  * k_i8_skinny: a workgroup takes 0.0125 us for a KiB of operands, and with r
+//    workgroups a CU these share its L1: 0.019 us a KiB and workgroup.
+//  * k_i8_gemm: a round of 256 x 256 tiles (one a CU) takes 0.8 us for 64 of k; a
+//    last round that would leave half of the chip idle is cut into 128 x 256
+//    pieces (0.26 us), one that would leave three quarters idle into 128 x 128
+//    pieces (0.204 us).  Where nothing is whole and the pieces leave CUs idle, K
+//    may be split: the integer sums cost a second launch and 0.86 us for a MB.
+I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
+  I8Choice best{1, {}};
+  double least = 1e30;
+  for (int t = 1; t <= 4; t *= 2) {
+    int64_t groups = 0;
+    for (int i = 0; i < count; ++i) groups += ceil_div(ns[i], 16 * t);
+    groups *= ceil_div(m, 16 * t);
+    const double r = (double)groups / 256, kib = 2.0 * t * 16 * k / 1024;
+    const double us = 2.5 + kib * (0.0125 + 0.019 * r) + (t == 1 ? 0.45 : t == 2 ? 1.5 : 3.4) * r;
+    if (us < least) least = us, best.skinny = t;
   }
-  return p;
+  I8Plan p{};
+  int64_t n = 0, pieces = 0;
+  for (int i = 0; i < count; ++i) {
+    p.nx += (int)ceil_div(ns[i], 256);
+    pieces += ceil_div(ns[i], 128) * ceil_div(m, 128);
+    n += ns[i];
+  }
+  p.ny = (int)ceil_div(m, 256);
+  const int64_t tiles = (int64_t)p.nx * p.ny, rest = tiles % 256;
+  const int slices = (int)(k / I8K);
+  p.whole = (int)(rest <= 128 ? tiles - rest : tiles);
+  p.cut = rest <= 64 ? 4 : 2;
+  if (p.whole > 0) pieces = rest * p.cut;
+  for (int ks = 1; ks <= 8; ++ks) {
+    if (ks > 1 && (p.whole > 0 || p.cut != 4 || slices < 8 * ks)) break;
+    p.per = (int)ceil_div(slices, ks);
+    p.ks = (int)ceil_div(slices, p.per);
+    double us = 3.3 + (double)(n + m) * k * 0.22e-6;
+    us += std::ceil(p.whole / 256.0) * (15.5 + 0.8 * slices);
+    if (p.whole < tiles) us += p.cut == 2 ? 11.4 + 0.26 * slices : std::ceil(pieces * p.ks / 256.0) * (2.3 + 0.204 * p.per);
+    if (p.ks > 1) us += 2.8 + 0.86e-6 * 4 * p.ks * m * n;
+    if (us < least) least = us, best.skinny = 0, best.plan = p;
+  }
+  return best;
 }
 
 }  // namespace
 
 size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
-  int tile_end[kGemvMaxGroup];
-  int end = 0;
+  const I8Choice c = choose(ns, count, k, m);
+  if (c.skinny != 0 || c.plan.ks == 1) return 0;
   int64_t n = 0;
-  for (int i = 0; i < count; ++i) {
-    end += (int)((ns[i] + 255) / 256);
-    tile_end[i] = end;
-    n += ns[i];
-  }
-  const I8Plan plan = plan_of(tile_end, count, k, m);
-  return plan.ks > 1 ? (size_t)plan.ks * (size_t)m * (size_t)n * sizeof(int) : 0;
+  for (int i = 0; i < count; ++i) n += ns[i];
+  return (size_t)c.plan.ks * (size_t)m * (size_t)n * sizeof(int);
 }
 
-hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows,
-                         int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void* work,
-                         hipStream_t s) {
+I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count) {
   I8Set set{};
   set.count = count;
-  int end = 0, most = 0;
   int64_t n = 0;
   for (int i = 0; i < count; ++i) {
     set.w[i] = reinterpret_cast<const int8_t*>(ws[i].packed);
@@ -425,26 +438,34 @@ hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ld
     set.rows[i] = out_rows[i];
     set.ldy[i] = ldys[i];
     set.n[i] = (int)ws[i].n;
-    end += (int)((ws[i].n + 255) / 256);
-    set.tile_end[i] = end;
     n += ws[i].n;
     set.n_end[i] = n;
+  }
+  return set;
+}
+
+hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
+                         const LoraEpi& lora, void* work, hipStream_t s) {
+  I8Set set = weights;
+  int64_t ns[kGemvMaxGroup];
+  int end = 0, most = 0;
+  for (int i = 0; i < set.count; ++i) {
+    ns[i] = set.n[i];
+    end += (int)ceil_div(set.n[i], 256);
+    set.tile_end[i] = end;
     most = std::max(most, set.n[i]);
   }
-  if (const char* e = getenv("I8SK")) {
-    int tn, tm;
-    if (sscanf(e, "%d,%d", &tn, &tm) == 2 && tn > 0) return launch_i8_skinny(set, tn, tm, Xq, xs, m, ws[0].k, lora, s);
-  }
-  const int k = (int)ws[0].k;
-  const I8Plan plan = plan_of(set.tile_end, count, k, m);
+  const I8Choice c = choose(ns, set.count, k, m);
+  if (c.skinny != 0) return launch_i8_skinny(set, c.skinny, Xq, xs, m, k, lora, s);
+  const I8Plan& plan = c.plan;
   int* part = plan.ks > 1 ? static_cast<int*>(work) : nullptr;
   const dim3 grid((unsigned)(plan.whole + (plan.nx * plan.ny - plan.whole) * plan.cut), (unsigned)plan.ks);
   if (lora.t != nullptr && plan.ks == 1)
-    hipLaunchKernelGGL(k_i8_gemm<true>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, k, lora, part);
+    hipLaunchKernelGGL(k_i8_gemm<true>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, (int)k, lora, part);
   else
-    hipLaunchKernelGGL(k_i8_gemm<false>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, k, lora, part);
+    hipLaunchKernelGGL(k_i8_gemm<false>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, (int)k, lora, part);
   if (part != nullptr)
-    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)((most + 1023) / 1024), (unsigned)m, (unsigned)count), dim3(256), 0, s,
+    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)ceil_div(most, 1024), (unsigned)m, (unsigned)set.count), dim3(256), 0, s,
                        set, part, plan.ks, xs, (int)m, lora);
   return hipGetLastError();
 }

@@ -23,8 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-
 // Eight consecutive values of a row as they are stored.
 template <typename T>
 struct Chunk8;
@@ -35,37 +33,29 @@ struct Chunk8<float> {
     a = *reinterpret_cast<const f32x4_t*>(p);
     b = *(reinterpret_cast<const f32x4_t*>(p) + 1);
   }
-  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
+    return m;
+  }
+  __device__ __forceinline__ uint2 codes(float s, bool finite) const {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[0] |= i8_code(a[i], s) << (8 * i);
+      w[1] |= i8_code(b[i], s) << (8 * i);
+    }
+    return finite ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+  }
 };
 template <>
 struct Chunk8<uint16_t> {
   u32x4_t v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
-  __device__ __forceinline__ float at(int i) const { return (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }
+  __device__ __forceinline__ uint32_t top() const { return i8_top_bf16(v); }
+  __device__ __forceinline__ uint2 codes(float s, bool finite) const { return i8_codes_bf16(v, s, finite); }
 };
-
-template <typename T>
-__device__ __forceinline__ uint32_t max_magnitude(const Chunk8<T>& c, uint32_t m) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(c.at(i)) & 0x7FFFFFFFu;
-    m = b > m ? b : m;
-  }
-  return m;
-}
-
-template <typename T>
-__device__ __forceinline__ u32x2_t codes_of(const Chunk8<T>& c, float s, bool finite) {
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // the quotient can pass 127 when s is subnormal and was rounded down
-    float q = __builtin_rintf(c.at(i) / s);
-    q = fminf(fmaxf(q, -127.f), 127.f);
-    w[i >> 2] |= ((uint32_t)(int)q & 0xFFu) << (8 * (i & 3));
-  }
-  return finite ? u32x2_t{w[0], w[1]} : u32x2_t{0u, 0u};
-}
 
 // One workgroup a row.  NC: chunks of 8 values a thread keeps (k <= 2048 * NC).
 template <typename T, int NC, bool KEEP>
@@ -85,36 +75,33 @@ __global__ __launch_bounds__(kThreads) void k_i8_quant_rows(const T* __restrict_
       if (tid + i * kThreads < chunks) c[i].load(x + 8 * (tid + i * kThreads));
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (tid + i * kThreads < chunks) m = max_magnitude(c[i], m);
+      if (tid + i * kThreads < chunks) m = max(m, c[i].top());
   } else {
     for (int i = tid; i < chunks; i += kThreads) {
       c[0].load(x + 8 * i);
-      m = max_magnitude(c[0], m);
+      m = max(m, c[0].top());
     }
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t t = __shfl_xor(m, o);
-    m = t > m ? t : m;
+    m = max(m, (uint32_t)__shfl_xor(m, o));
   }
   if ((tid & 63) == 0) red[tid >> 6] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) m = red[i] > m ? red[i] : m;
-  const bool finite = m < 0x7F800000u;
-  float s = __uint_as_float(m) / 127.f;
-  if (s == 0.f) s = 1.f;
-  if (!finite) s = __uint_as_float(0x7FC00000u);
+  for (int i = 0; i < kThreads / 64; ++i) m = max(m, red[i]);
+  bool finite;
+  const float s = i8_scale(m, finite);
   if (tid == 0) scales[row] = s;
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
       if (tid + i * kThreads < chunks)
-        *reinterpret_cast<u32x2_t*>(q + 8 * (tid + i * kThreads)) = codes_of(c[i], s, finite);
+        *reinterpret_cast<uint2*>(q + 8 * (tid + i * kThreads)) = c[i].codes(s, finite);
   } else {
     for (int i = tid; i < chunks; i += kThreads) {
       c[0].load(x + 8 * i);
-      *reinterpret_cast<u32x2_t*>(q + 8 * i) = codes_of(c[0], s, finite);
+      *reinterpret_cast<uint2*>(q + 8 * i) = c[0].codes(s, finite);
     }
   }
 }
@@ -133,11 +120,11 @@ __global__ __launch_bounds__(kThreads) void k_i8_dequant(const int8_t* __restric
   const int8_t* q = Q + row * k;
   uint16_t* o = out + row * k;
   for (int i = 8 * threadIdx.x; i < k; i += 8 * kThreads) {
-    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(q + i);
+    const uint2 v = *reinterpret_cast<const uint2*>(q + i);
     uint32_t d[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t w = v[j >> 1] >> (16 * (j & 1));
+      const uint32_t w = (j < 2 ? v.x : v.y) >> (16 * (j & 1));
       d[j] = cvt_pk_bf16((float)(int8_t)(uint8_t)w * s, (float)(int8_t)(uint8_t)(w >> 8) * s);
     }
     *reinterpret_cast<u32x4_t*>(o + i) = u32x4_t{d[0], d[1], d[2], d[3]};

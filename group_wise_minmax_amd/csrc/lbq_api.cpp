@@ -263,20 +263,23 @@ size_t align16(size_t b) { return (b + 15) / 16 * 16; }
 
 // Workspace of the forward of INT8 weights that share X (16-byte aligned
 // pieces): the tokens' codes [m][k] and scales [m], then what the product
-// takes.
+// takes; none where one launch quantizes and multiplies.
 size_t i8_token_bytes(int64_t m, int64_t k) { return align16((size_t)m * (size_t)k) + align16((size_t)m * sizeof(float)); }
 size_t i8_workspace(const int64_t* ns, int count, int64_t k, int64_t m) {
+  if (lbq::i8_decode_fits(m, k)) return 0;
   return i8_token_bytes(m, k) + lbq::i8_fwd_workspace_bytes(ns, count, k, m);
 }
 hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* rows, int count,
                   const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, void* ws, hipStream_t s) {
   const int64_t k = w[0].k;
+  const lbq::I8Set set = lbq::i8_set(w, ys, ldys, rows, count);
+  if (lbq::i8_decode_fits(m, k)) return lbq::launch_i8_decode(set, X, m, k, lora, s);
   uint8_t* p = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(p);
   float* xs = reinterpret_cast<float*>(p + align16((size_t)m * (size_t)k));
   const hipError_t e = lbq::launch_i8_quant_bf16(X, m, k, k, xq, xs, s);
   if (e != hipSuccess) return e;
-  return lbq::launch_i8_fwd(w, ys, ldys, rows, count, xq, xs, m, lora, p + i8_token_bytes(m, k), s);
+  return lbq::launch_i8_fwd(set, xq, xs, m, k, lora, p + i8_token_bytes(m, k), s);
 }
 
 hipError_t dispatch_fwd(const lbq_desc* desc, const lbq::WView& w, const uint16_t* X, int64_t m,
@@ -455,7 +458,7 @@ lbq_status lbq_linear_fwd_tokens(const lbq_desc* desc, const lbq_qtensor* q, con
   }
   const lbq::LoraEpi none{nullptr, nullptr, 0, 0};
   const lbq::WView w = view_of(desc, q);
-  return hip_status(lbq::launch_i8_fwd(&w, &Y, &ldy, &q->out_rows, 1, Xq, xscale, m, none, workspace,
+  return hip_status(lbq::launch_i8_fwd(lbq::i8_set(&w, &Y, &ldy, &q->out_rows, 1), Xq, xscale, m, desc->k, none, workspace,
                                        static_cast<hipStream_t>(stream)),
                     "lbq_linear_fwd_tokens");
 }

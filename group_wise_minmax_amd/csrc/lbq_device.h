@@ -65,6 +65,13 @@ __device__ __forceinline__ i32x4_t mfma_i8(const i32x4_t& a, const i32x4_t& b, c
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// LDS tiles of 64-byte rows of 8-bit codes.
+// Chunk c (16 bytes) of row r lies at position c ^ key(r): the 16 lanes that a
+// 16-byte LDS read serves together (0-3, 12-15, 20-23 and 24-27 of a half wave,
+// or the other 16) then read 16 different sixteenths of the 64 banks, where
+// lane l reads chunk l / 16 of row l % 16.
+__device__ __forceinline__ int i8_key(int r) { return -(r >> 2) & 3; }
+
 // Sum over the 64 lanes of a wave, result in every lane: four DPP steps
 // (xor 1, xor 2 within quads, half-row and row mirrors) and two cross-row
 // exchanges.
@@ -135,6 +142,15 @@ __device__ __forceinline__ void tile_at(int t, int nx, int ny, int& tx, int& ty)
   const int r = t - group * GM * nx;
   ty = first + r % gm;
   tx = r / gm;
+}
+
+// 16 bytes a lane from r (byte offset voff of the lane plus soff) to LDS: lane
+// l's at `lds` + 16 l, `lds` the same in the whole wave.  (The host pass knows
+// no 16-byte form of the builtin.)
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int8_t* lds, int voff, int soff) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+#endif
 }
 
 // Tile index of workgroup `bid` among nx * ny tiles, XCD-aware and grouped.
@@ -319,6 +335,42 @@ __device__ __forceinline__ float nf4_block_scale(const WView& w, int64_t blk, fl
 
 // bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
 __device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
+
+// 8-bit quantization of a row (k_i8_quant.hip has the rule).  Magnitudes are
+// compared as integers, the fp32 bits without the sign.
+// Largest magnitude of eight bf16 values.
+__device__ __forceinline__ uint32_t i8_top_bf16(const u32x4_t& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = (v[i] & 0x7FFFu) << 16, hi = v[i] & 0x7FFF0000u;
+    m = m > lo ? m : lo;
+    m = m > hi ? m : hi;
+  }
+  return m;
+}
+// The scale of a row of largest magnitude `top`; whether the row is finite.
+__device__ __forceinline__ float i8_scale(uint32_t top, bool& finite) {
+  finite = top < 0x7F800000u;
+  float s = __uint_as_float(top) / 127.f;
+  if (s == 0.f) s = 1.f;
+  return finite ? s : __uint_as_float(0x7FC00000u);
+}
+// Code of x in the low byte.  (The quotient can pass 127 when s is subnormal
+// and was rounded down.)
+__device__ __forceinline__ uint32_t i8_code(float x, float s) {
+  const float q = fminf(fmaxf(__builtin_rintf(x / s), -127.f), 127.f);
+  return (uint32_t)(int)q & 0xFFu;
+}
+// Codes of eight bf16 values; zeros in a row that is not finite.
+__device__ __forceinline__ uint2 i8_codes_bf16(const u32x4_t& v, float s, bool finite) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    w[h] = i8_code(bf16_lo(v[2 * h]), s) | i8_code(bf16_hi(v[2 * h]), s) << 8 |
+           i8_code(bf16_lo(v[2 * h + 1]), s) << 16 | i8_code(bf16_hi(v[2 * h + 1]), s) << 24;
+  return finite ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+}
 
 // Outputs of channels nb .. nb + 3 (nb < n) of weight wi and token mr from their
 // integer sums: scaled (one rounding to fp32 each: the caller's file has

@@ -191,18 +191,21 @@ struct I8Set {
   int64_t n_end[kGemvMaxGroup];  // channels of weights 0 .. i
   int count;
 };
+I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count);
 // The product on quantized tokens Xq [m][k] with scales xs [m], for up to
 // kGemvMaxGroup weights of one k (the LoRA term only with count 1).  `work`
 // holds i8_fwd_workspace_bytes() bytes.
 size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m);
-hipError_t launch_i8_fwd(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows,
-                         int count, const int8_t* Xq, const float* xs, int64_t m, const LoraEpi& lora, void* work,
-                         hipStream_t s);
-
-// The same by workgroups of 16 tn channels and 16 tm tokens (tn, tm in {1, 2, 4})
-// that split K over their waves; set.tile_end is not looked at.
-hipError_t launch_i8_skinny(const I8Set& set, int tn, int tm, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
+hipError_t launch_i8_fwd(const I8Set& set, const int8_t* Xq, const float* xs, int64_t m, int64_t k, const LoraEpi& lora,
+                         void* work, hipStream_t s);
+// The same by workgroups of 16 t channels and 16 t tokens (t = 1, 2, 4) that
+// split K over their waves; set.tile_end is not looked at.
+hipError_t launch_i8_skinny(const I8Set& set, int t, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
                             const LoraEpi& lora, hipStream_t s);
+// From bf16 tokens X [m][k] in one launch: m <= 4 and m * k <= kI8DecodeCodes.
+constexpr int kI8DecodeCodes = 16384;
+inline bool i8_decode_fits(int64_t m, int64_t k) { return m <= 4 && m * k <= kI8DecodeCodes; }
+hipError_t launch_i8_decode(const I8Set& set, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora, hipStream_t s);
 
 // ---- gradient norm (k_grad.hip) -------------------------------------------------
 // Tensors of one launch, in the kernel's arguments (they may take 4 KiB).
