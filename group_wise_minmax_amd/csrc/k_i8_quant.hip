@@ -10,9 +10,9 @@
 // so a row that holds an infinity or a NaN is seen as such: it gets the scale
 // NaN and codes 0, and only that token's outputs are NaN.
 //
-// Bound by memory: a row is read once and kept in registers between the
-// search for its largest magnitude and the division, up to 8192 values
-// (fp32) or 16384 (bf16) a workgroup; a longer row is read again, from L2.
+// Bound by memory: a row of up to 32768 values is read once and kept in registers
+// between the search for its largest magnitude and the codes; a longer row is
+// read again, from L2.
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"
@@ -39,14 +39,8 @@ struct Chunk8<float> {
     for (int i = 0; i < 4; ++i) m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
     return m;
   }
-  __device__ __forceinline__ uint2 codes(float s, bool finite) const {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[0] |= i8_code(a[i], s) << (8 * i);
-      w[1] |= i8_code(b[i], s) << (8 * i);
-    }
-    return finite ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+  __device__ __forceinline__ uint2 codes(float s, float rs, bool finite) const {
+    return i8_codes([&](int i) { return i < 4 ? a[i] : b[i - 4]; }, s, rs, finite);
   }
 };
 template <>
@@ -54,14 +48,15 @@ struct Chunk8<uint16_t> {
   u32x4_t v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
   __device__ __forceinline__ uint32_t top() const { return i8_top_bf16(v); }
-  __device__ __forceinline__ uint2 codes(float s, bool finite) const { return i8_codes_bf16(v, s, finite); }
+  __device__ __forceinline__ uint2 codes(float s, float rs, bool finite) const { return i8_codes_bf16(v, s, rs, finite); }
 };
 
-// One workgroup a row.  NC: chunks of 8 values a thread keeps (k <= 2048 * NC).
-template <typename T, int NC, bool KEEP>
-__global__ __launch_bounds__(kThreads) void k_i8_quant_rows(const T* __restrict__ X, int64_t ldx, int64_t k,
-                                                           int8_t* __restrict__ Q, float* __restrict__ scales) {
-  __shared__ uint32_t red[kThreads / 64];
+// One workgroup of NT threads a row.  NC: chunks of 8 values a thread keeps
+// (k <= 8 * NT * NC).
+template <typename T, int NT, int NC, bool KEEP>
+__global__ __launch_bounds__(NT) void k_i8_quant_rows(const T* __restrict__ X, int64_t ldx, int64_t k,
+                                                     int8_t* __restrict__ Q, float* __restrict__ scales) {
+  __shared__ uint32_t red[NT / 64];
   const int64_t row = blockIdx.x;
   const T* x = X + row * ldx;
   int8_t* q = Q + row * k;
@@ -72,12 +67,12 @@ __global__ __launch_bounds__(kThreads) void k_i8_quant_rows(const T* __restrict_
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (tid + i * kThreads < chunks) c[i].load(x + 8 * (tid + i * kThreads));
+      if (tid + i * NT < chunks) c[i].load(x + 8 * (tid + i * NT));
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (tid + i * kThreads < chunks) m = max(m, c[i].top());
+      if (tid + i * NT < chunks) m = max(m, c[i].top());
   } else {
-    for (int i = tid; i < chunks; i += kThreads) {
+    for (int i = tid; i < chunks; i += NT) {
       c[0].load(x + 8 * i);
       m = max(m, c[0].top());
     }
@@ -89,27 +84,40 @@ __global__ __launch_bounds__(kThreads) void k_i8_quant_rows(const T* __restrict_
   if ((tid & 63) == 0) red[tid >> 6] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) m = max(m, red[i]);
+  for (int i = 0; i < NT / 64; ++i) m = max(m, red[i]);
   bool finite;
-  const float s = i8_scale(m, finite);
+  const float s = i8_scale(m, finite), rs = 1.f / s;
   if (tid == 0) scales[row] = s;
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (tid + i * kThreads < chunks)
-        *reinterpret_cast<uint2*>(q + 8 * (tid + i * kThreads)) = c[i].codes(s, finite);
+      if (tid + i * NT < chunks)
+        *reinterpret_cast<uint2*>(q + 8 * (tid + i * NT)) = c[i].codes(s, rs, finite);
   } else {
-    for (int i = tid; i < chunks; i += kThreads) {
+    for (int i = tid; i < chunks; i += NT) {
       c[0].load(x + 8 * i);
-      *reinterpret_cast<uint2*>(q + 8 * i) = c[0].codes(s, finite);
+      *reinterpret_cast<uint2*>(q + 8 * i) = c[0].codes(s, rs, finite);
     }
   }
 }
 
-template <typename T, int NC, bool KEEP>
+template <int NT, int NC, bool KEEP, typename T>
 hipError_t launch_rows(const T* X, int64_t rows, int64_t k, int64_t ldx, int8_t* Q, float* scales, hipStream_t s) {
-  hipLaunchKernelGGL((k_i8_quant_rows<T, NC, KEEP>), dim3((unsigned)rows), dim3(kThreads), 0, s, X, ldx, k, Q, scales);
+  hipLaunchKernelGGL((k_i8_quant_rows<T, NT, NC, KEEP>), dim3((unsigned)rows), dim3(NT), 0, s, X, ldx, k, Q, scales);
   return hipGetLastError();
+}
+
+// At most two chunks a thread where the workgroup can be that large: a row's
+// time is its latency (3 rows of 28672: 256 threads that read the row twice
+// 14.8 us).
+template <typename T>
+hipError_t launch_quant(const T* X, int64_t rows, int64_t k, int64_t ldx, int8_t* Q, float* scales, hipStream_t s) {
+  if (k <= 2048) return launch_rows<256, 1, true>(X, rows, k, ldx, Q, scales, s);
+  if (k <= 4096) return launch_rows<256, 2, true>(X, rows, k, ldx, Q, scales, s);
+  if (k <= 8192) return launch_rows<512, 2, true>(X, rows, k, ldx, Q, scales, s);
+  if (k <= 16384) return launch_rows<1024, 2, true>(X, rows, k, ldx, Q, scales, s);
+  if (k <= 32768) return launch_rows<1024, 4, true>(X, rows, k, ldx, Q, scales, s);
+  return launch_rows<1024, 1, false>(X, rows, k, ldx, Q, scales, s);
 }
 
 __global__ __launch_bounds__(kThreads) void k_i8_dequant(const int8_t* __restrict__ Q,
@@ -134,19 +142,12 @@ __global__ __launch_bounds__(kThreads) void k_i8_dequant(const int8_t* __restric
 }  // namespace
 
 hipError_t launch_i8_quant_f32(const float* W, int64_t n, int64_t k, int8_t* Q, float* scales, hipStream_t s) {
-  if (k <= 2048) return launch_rows<float, 1, true>(W, n, k, k, Q, scales, s);
-  if (k <= 4096) return launch_rows<float, 2, true>(W, n, k, k, Q, scales, s);
-  if (k <= 8192) return launch_rows<float, 4, true>(W, n, k, k, Q, scales, s);
-  return launch_rows<float, 1, false>(W, n, k, k, Q, scales, s);
+  return launch_quant(W, n, k, k, Q, scales, s);
 }
 
 hipError_t launch_i8_quant_bf16(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Q, float* scales,
                                 hipStream_t s) {
-  if (k <= 2048) return launch_rows<uint16_t, 1, true>(X, m, k, ldx, Q, scales, s);
-  if (k <= 4096) return launch_rows<uint16_t, 2, true>(X, m, k, ldx, Q, scales, s);
-  if (k <= 8192) return launch_rows<uint16_t, 4, true>(X, m, k, ldx, Q, scales, s);
-  if (k <= 16384) return launch_rows<uint16_t, 8, true>(X, m, k, ldx, Q, scales, s);
-  return launch_rows<uint16_t, 1, false>(X, m, k, ldx, Q, scales, s);
+  return launch_quant(X, m, k, ldx, Q, scales, s);
 }
 
 hipError_t launch_i8_dequant(const WView& w, uint16_t* out, hipStream_t s) {

@@ -222,11 +222,11 @@ __global__ __launch_bounds__(kThreads) void k_i8_decode(I8Set set, const uint16_
     return t;
   };
   bool finite;
-  const float s = i8_scale(top_of(row), finite);
+  const float s = i8_scale(top_of(row), finite), rs = 1.f / s;
 #pragma unroll
   for (int i = 0; i < kDecodeChunks; ++i)
     if (first + i * stride < chunks)
-      *reinterpret_cast<uint2*>(codes + row * k + 8 * (first + i * stride)) = i8_codes_bf16(c[i], s, finite);
+      *reinterpret_cast<uint2*>(codes + row * k + 8 * (first + i * stride)) = i8_codes_bf16(c[i], s, rs, finite);
   barrier_lds();
 
   i32x4_t acc = {0, 0, 0, 0};
