@@ -366,9 +366,12 @@ def lbq_linear_fwd_grouped(X: torch.Tensor, qws, outs=None, workspace: Optional[
     return outs
 
 
-def lbq_linear_bwd_dx(dY: torch.Tensor, qw: QuantizedWeight,
-                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """dX = dY . deq(W) in bf16 (see ``lbq_linear_bwd_dx`` in lbq.h)."""
+def lbq_linear_bwd_dx(dY: torch.Tensor, qw: QuantizedWeight, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX = dY . deq(W) in bf16 (see ``lbq_linear_bwd_dx`` in lbq.h; an INT8
+    weight runs as ``lbq_linear_bwd_dx_grouped_ws``)."""
+    if qw.desc.format == LBQ_INT8:
+        return lbq_linear_bwd_dx_grouped([dY], [qw], out, workspace)
     _need(dY, "dY", torch.bfloat16)
     if dY.dim() != 2 or dY.shape[1] != qw.n:
         raise ValueError(f"dY must be [m, {qw.n}]")
@@ -384,9 +387,15 @@ def lbq_linear_bwd_dx(dY: torch.Tensor, qw: QuantizedWeight,
     return out
 
 
-def lbq_linear_bwd_dx_grouped(dYs, qws, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def lbq_linear_bwd_dx_grouped_workspace_bytes(qws, m: int) -> int:
+    descs = (Desc * len(qws))(*[q.desc for q in qws])
+    return lib.lbq_linear_bwd_dx_grouped_workspace_bytes(len(qws), descs, m)
+
+
+def lbq_linear_bwd_dx_grouped(dYs, qws, out: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = sum_i dYs[i] . deq(W_i) in bf16 for weights of one format that
-    share X and k (see ``lbq_linear_bwd_dx_grouped`` in lbq.h)."""
+    share X and k (see ``lbq_linear_bwd_dx_grouped_ws`` in lbq.h)."""
     qws, dYs = list(qws), list(dYs)
     count = len(qws)
     if not 1 <= count <= LBQ_MAX_GROUP or len(dYs) != count:
@@ -404,10 +413,13 @@ def lbq_linear_bwd_dx_grouped(dYs, qws, out: Optional[torch.Tensor] = None) -> t
     descs = (Desc * count)(*[q.desc for q in qws])
     qts = (QTensor * count)(*[q.qtensor() for q in qws])
     dps = (ctypes.c_void_p * count)(*[d.data_ptr() for d in dYs])
-    _same_device(dYs[0].device, out, *dYs, *[q.packed for q in qws])
+    if workspace is None:
+        workspace = _ws(lib.lbq_linear_bwd_dx_grouped_workspace_bytes(count, descs, m), dYs[0].device)
+    _same_device(dYs[0].device, out, workspace, *dYs, *[q.packed for q in qws])
     with _on(dYs[0].device):
-        check(lib.lbq_linear_bwd_dx_grouped(count, descs, qts, dps, m, out.data_ptr(), _stream(dYs[0].device)),
-              "lbq_linear_bwd_dx_grouped")
+        check(lib.lbq_linear_bwd_dx_grouped_ws(count, descs, qts, dps, m, out.data_ptr(), _ptr(workspace),
+                                               0 if workspace is None else workspace.numel(), _stream(dYs[0].device)),
+              "lbq_linear_bwd_dx_grouped_ws")
     return out
 
 

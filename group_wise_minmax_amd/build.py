@@ -34,10 +34,11 @@ COMMON = [
 # registers would cost an extra move each.
 PER_FILE = {"k_quant.hip": ["-ffp-contract=off"],
             "k_i8_quant.hip": ["-ffp-contract=off"], "k_i8_gemm.hip": ["-ffp-contract=off"],
-            "k_i8_skinny.hip": ["-ffp-contract=off"],
+            "k_i8_skinny.hip": ["-ffp-contract=off"], "k_i8_dx.hip": ["-ffp-contract=off"],
             "k_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 SOURCES = ["lbq_api.cpp", "k_quant.hip", "k_gemv1.hip", "k_skinny.hip", "k_gemm_fwd.hip", "k_bwd.hip", "k_lora.hip",
-           "k_noalloc.hip", "k_i8_quant.hip", "k_i8_gemm.hip", "k_i8_skinny.hip", "k_grad.hip"]
+           "k_noalloc.hip", "k_i8_quant.hip", "k_i8_gemm.hip", "k_i8_skinny.hip", "k_i8_dx.hip",
+           "k_grad.hip"]
 
 
 def hipcc() -> str:

@@ -208,6 +208,7 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   float md_s;
   int md_i;
   float md_off = 0.f;  // the loaded stage's weight's offset (the binding may move on before the store)
+  int left = BNR;      // 8-bit: rows of the weight from the loaded stage on
   // loads of the stage starting at row vt of the set, from the bound weight
   auto load_stage = [&](int64_t vt) {
     const int st = (int)(vt / BNR);
@@ -215,6 +216,7 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     const __amdgpu_buffer_rsrc_t r_w = b.w, r_d = b.d, r_s = b.s, r_z = b.z;
     const int64_t Nw = b.n;
     const int64_t nt = (int64_t)(st - b.beg) * BNR;
+    if constexpr (T::fmt == FMT_INT8) left = (int)(Nw - nt);
     const uint32_t d_voff = (uint32_t)((d_row * Nw + d_col) * 2);
 #pragma unroll
     for (int i = 0; i < DCH; ++i) {
@@ -254,6 +256,14 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   };
   auto store_stage = [&](int buf) {
     char* ds = ds_base + buf * DS_BUF;
+    if constexpr (T::fmt == FMT_INT8) {
+      // dY past a token's last row is the next token's: cleared, so that an
+      // infinity or a NaN there stays out of this token's zero weights
+      if (left < BNR && d_col >= left) {
+#pragma unroll
+        for (int i = 0; i < DCH; ++i) dr[i] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+    }
 #pragma unroll
     for (int i = 0; i < DCH; ++i) {
       const int ci = tid + NT * i;
@@ -344,7 +354,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   };
 
   // n % 8 == 0, so the rows of a weight's last 64-wide stage past its n only
-  // meet zero weights (buffer reads past the end) times finite dY values.
+  // meet zero weights (buffer reads past the end) times finite dY values (8-bit
+  // weights: times zeros, see store_stage).
   if constexpr (T::fmt == FMT_NF4) __syncthreads();  // pair table visible
   load_stage(0);
   store_stage(0);
@@ -519,7 +530,6 @@ BwdSet make_bwd_set(const WView* ws, const uint16_t* const* dys, int count) {
 
 hipError_t launch_bwd_dx(WKind kind, const WView& w, const uint16_t* dY, int64_t m,
                          uint16_t* dX, const LoraDx& lora, const Nf4Table& tab, hipStream_t s) {
-  if (kind == WK_I8) return BwdLauncher<WK_I8>::run(make_bwd_set(&w, &dY, 1), m, dX, lora, tab, s);
   return dispatch_kind<BwdLauncher>(kind, make_bwd_set(&w, &dY, 1), m, dX, lora, tab, s);
 }
 
@@ -529,9 +539,20 @@ hipError_t launch_bwd_dx_set(WKind kind, const WView* ws, const uint16_t* const*
   for (int i = 1; i < count; ++i)
     if (ws[i].k != ws[0].k) return hipErrorInvalidValue;
   const LoraDx none{nullptr, nullptr, 0, 0};
-  if (kind == WK_I8) return BwdLauncher<WK_I8>::run(make_bwd_set(ws, dys, count), m, dX, none, tab, s);
   return dispatch_kind<BwdLauncher>(kind, make_bwd_set(ws, dys, count), m, dX, none, tab, s);
 }
 
+hipError_t launch_bwd_dx_i8_tiles(const WView* ws, const uint16_t* const* dys, int count, int bk, int bm, int64_t m,
+                                  uint16_t* dX, const LoraDx& lora, hipStream_t s) {
+  const BwdSet set = make_bwd_set(ws, dys, count);
+  const Nf4Table none{};
+  // several rounds of 256 x 256 tiles are cut as for the other formats
+  const int64_t t256 = ((ws[0].k + 255) / 256) * ((m + 255) / 256);
+  if (bk == 256 && bm == 256 && t256 > 256) return BwdLauncher<WK_I8>::run(set, m, dX, lora, none, s);
+  if (bk == 256 && bm == 256) return launch_bwd_cfg<WK_I8, 256, 256, 2, 4>(set, m, dX, lora, none, s);
+  if (bk == 256 && bm == 128) return launch_bwd_cfg<WK_I8, 256, 128, 4, 2>(set, m, dX, lora, none, s);
+  if (bk == 128 && bm == 128) return launch_bwd_cfg<WK_I8, 128, 128, 2, 2>(set, m, dX, lora, none, s);
+  return hipErrorInvalidValue;
+}
 
 }  // namespace lbq

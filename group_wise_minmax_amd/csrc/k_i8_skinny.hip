@@ -46,58 +46,11 @@ __device__ __forceinline__ int slices_of(int wave, int k) {
 }
 __device__ __forceinline__ int slice_at(int wave, int j) { return 128 * (wave + kWaves * (j >> 1)) + 64 * (j & 1); }
 
-// Waits for all loads but the last `N` (0 to 15), or for all LDS reads, with no
-// memory access moved across.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 16, "vmcnt's low four bits");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | N);
-  asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void wait_reads() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);
-  asm volatile("" ::: "memory");
-}
-
 // Barrier for LDS alone: loads of weights stay on their way.
 __device__ __forceinline__ void barrier_lds() {
   asm volatile("" ::: "memory");
   lds_barrier();
   asm volatile("" ::: "memory");
-}
-
-// A wave's `cnt` slices through a ring of U slots, N loads a slice:
-// load(slot, slice) issues them, mma(slot, slice) reads the slot and multiplies.
-template <int U, int N, typename L, typename M>
-__device__ __forceinline__ void run_ring(int cnt, L load, M mma) {
-  int j = 0;
-  for (; j + 2 * U <= cnt; j += U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      wait_loads<(U - 1) * N>();
-      mma(u, j + u);
-      wait_reads();
-      load(u, j + U + u);
-    }
-  }
-  // the last slices: U of them on their way, up to U - 1 after those
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (j + u < cnt) {
-      wait_loads<0>();
-      mma(u, j + u);
-      wait_reads();
-      if (j + U + u < cnt) load(u, j + U + u);
-    }
-  }
-  j += U;
-  wait_loads<0>();
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (j + u < cnt) mma(u, j + u);
-  wait_reads();
 }
 
 template <int T, int U>

@@ -310,6 +310,17 @@ size_t fwd_workspace(const lbq_desc* desc, int64_t m, bool lora) {
   return 0;
 }
 
+// Input gradient of INT8 weights, checked (m >= 1).
+lbq_status i8_bwd(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs, const uint16_t* const* dYs, int64_t m,
+                  uint16_t* dX, void* workspace, size_t ws_bytes, void* stream, const char* who) {
+  lbq::WView ws[LBQ_MAX_GROUP];
+  for (int32_t i = 0; i < count; ++i) ws[i] = view_of(&descs[i], &qs[i]);
+  const lbq::LoraDx none{nullptr, nullptr, 0, 0};
+  return hip_status(lbq::launch_i8_dx(ws, dYs, count, m, dX, none, static_cast<float*>(workspace), ws_bytes,
+                                      static_cast<hipStream_t>(stream)),
+                    who);
+}
+
 // Checks shared by the two input-gradient entries (m == 0 passes).
 lbq_status check_bwd_common(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* dY,
                             int64_t m, uint16_t* dX, const char* who) {
@@ -656,32 +667,56 @@ lbq_status lbq_linear_bwd_dx(const lbq_desc* desc, const lbq_qtensor* q, const u
                              int64_t m, uint16_t* dX, void* stream) {
   lbq_status st = check_bwd_common(desc, q, dY, m, dX, "lbq_linear_bwd_dx");
   if (st != LBQ_OK || m == 0) return st == LBQ_OK ? ok() : st;
+  if (desc->format == LBQ_INT8) return i8_bwd(1, desc, q, &dY, m, dX, nullptr, 0, stream, "lbq_linear_bwd_dx");
   const lbq::LoraDx none{nullptr, nullptr, 0, 0};
   return hip_status(lbq::launch_bwd_dx(kind_of(desc), view_of(desc, q), dY, m, dX, none, nf4_table(),
                                        static_cast<hipStream_t>(stream)),
                     "lbq_linear_bwd_dx");
 }
 
-lbq_status lbq_linear_bwd_dx_grouped(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
-                                     const uint16_t* const* dYs, int64_t m, uint16_t* dX, void* stream) {
+size_t lbq_linear_bwd_dx_grouped_workspace_bytes(int32_t count, const lbq_desc* descs, int64_t m) {
+  if (count < 1 || count > LBQ_MAX_GROUP || descs == nullptr || m < 1) return 0;
+  int64_t ns[LBQ_MAX_GROUP];
+  for (int32_t i = 0; i < count; ++i) {
+    if (check_desc(&descs[i]) != LBQ_OK || descs[i].k != descs[0].k || descs[i].format != LBQ_INT8) return 0;
+    ns[i] = descs[i].n;
+  }
+  return lbq::i8_dx_workspace_bytes(ns, count, descs[0].k, m);
+}
+
+static lbq_status bwd_grouped(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs, const uint16_t* const* dYs,
+                              int64_t m, uint16_t* dX, void* workspace, size_t ws_bytes, void* stream, const char* who) {
   if (count < 1 || count > LBQ_MAX_GROUP)
     return fail(LBQ_E_SHAPE, "count must be in [1, %d] (got %d)", LBQ_MAX_GROUP, count);
   if (descs == nullptr || qs == nullptr || dYs == nullptr) return fail(LBQ_E_NULL, "descs, qs and dYs must be non-NULL");
   for (int32_t i = 0; i < count; ++i) {
-    const lbq_status st = check_bwd_common(&descs[i], &qs[i], dYs[i], m, dX, "lbq_linear_bwd_dx_grouped");
+    const lbq_status st = check_bwd_common(&descs[i], &qs[i], dYs[i], m, dX, who);
     if (st != LBQ_OK) return st;
     if (descs[i].k != descs[0].k)
       return fail(LBQ_E_SHAPE, "weight %d has k = %lld, weight 0 has %lld", i, (long long)descs[i].k,
                   (long long)descs[0].k);
     if (kind_of(&descs[i]) != kind_of(&descs[0]))
-      return fail(LBQ_E_UNSUPPORTED, "lbq_linear_bwd_dx_grouped takes weights of one format (weight %d differs)", i);
+      return fail(LBQ_E_UNSUPPORTED, "%s takes weights of one format (weight %d differs)", who, i);
   }
+  if (workspace != nullptr && !aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
   if (m == 0) return ok();
+  if (descs[0].format == LBQ_INT8) return i8_bwd(count, descs, qs, dYs, m, dX, workspace, ws_bytes, stream, who);
   lbq::WView ws[LBQ_MAX_GROUP];
   for (int32_t i = 0; i < count; ++i) ws[i] = view_of(&descs[i], &qs[i]);
   return hip_status(lbq::launch_bwd_dx_set(kind_of(&descs[0]), ws, dYs, count, m, dX, nf4_table(),
                                            static_cast<hipStream_t>(stream)),
-                    "lbq_linear_bwd_dx_grouped");
+                    who);
+}
+
+lbq_status lbq_linear_bwd_dx_grouped(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
+                                     const uint16_t* const* dYs, int64_t m, uint16_t* dX, void* stream) {
+  return bwd_grouped(count, descs, qs, dYs, m, dX, nullptr, 0, stream, "lbq_linear_bwd_dx_grouped");
+}
+
+lbq_status lbq_linear_bwd_dx_grouped_ws(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
+                                        const uint16_t* const* dYs, int64_t m, uint16_t* dX, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  return bwd_grouped(count, descs, qs, dYs, m, dX, workspace, ws_bytes, stream, "lbq_linear_bwd_dx_grouped_ws");
 }
 
 // LoRA backward workspace: Bt [rp][n], G [m][rp], Gt and Tt [rp][mp] (bf16),
@@ -691,8 +726,10 @@ size_t lbq_lora_bwd_workspace_bytes(const lbq_desc* desc, int64_t m, int32_t r) 
   const size_t rp = (size_t)round_rank(r);
   const size_t mp = (size_t)round_rows(m);
   // the two adapter products run together, then the two outer products
-  const size_t part = std::max(lbq::lora_xa_part_bytes(m, desc->n, r) + lbq::lora_xa_part_bytes(m, desc->k, r),
-                               lbq::lora_outer_part_bytes(m, desc->k, r) + lbq::lora_outer_part_bytes(m, desc->n, r));
+  size_t part = std::max(lbq::lora_xa_part_bytes(m, desc->n, r) + lbq::lora_xa_part_bytes(m, desc->k, r),
+                         lbq::lora_outer_part_bytes(m, desc->k, r) + lbq::lora_outer_part_bytes(m, desc->n, r));
+  // between them the input gradient, whose reduction may be split (INT8)
+  if (desc->format == LBQ_INT8) part = std::max(part, lbq::i8_dx_workspace_bytes(&desc->n, 1, desc->k, m));
   return align16(rp * (size_t)desc->n * 2) + align16((size_t)m * rp * 2) + 2 * align16(rp * mp * 2) + align16(part);
 }
 
@@ -745,7 +782,12 @@ lbq_status lbq_lora_bwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
   }
   if (e != hipSuccess) return hip_status(e, "lbq_lora_bwd (adapter products)");
   const lbq::LoraDx lora{G, A, r, rp};
-  e = lbq::launch_bwd_dx(kind_of(desc), view_of(desc, q), dY, m, dX, lora, nf4_table(), s);
+  if (desc->format == LBQ_INT8) {
+    const lbq::WView w = view_of(desc, q);
+    e = lbq::launch_i8_dx(&w, &dY, 1, m, dX, lora, part, lbq::i8_dx_workspace_bytes(&desc->n, 1, desc->k, m), s);
+  } else {
+    e = lbq::launch_bwd_dx(kind_of(desc), view_of(desc, q), dY, m, dX, lora, nf4_table(), s);
+  }
   if (e != hipSuccess) return hip_status(e, "lbq_lora_bwd (input gradient)");
   {
     const uint16_t* pts[2] = {Gt, Tt};

@@ -153,6 +153,53 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, int8_t* ld
 #endif
 }
 
+// Waits for all loads but the last `N`, or for all LDS reads, with no
+// memory access moved across.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt has six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+}
+
+// A wave's `cnt` slices through a ring of U slots, N loads a slice:
+// load(slot, slice) issues them, mma(slot, slice) reads the slot and multiplies.
+template <int U, int N, typename L, typename M>
+__device__ __forceinline__ void run_ring(int cnt, L load, M mma) {
+  int j = 0;
+  for (; j + 2 * U <= cnt; j += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      wait_loads<(U - 1) * N>();
+      mma(u, j + u);
+      wait_reads();
+      load(u, j + U + u);
+    }
+  }
+  // the last slices: U of them on their way, up to U - 1 after those
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (j + u < cnt) {
+      wait_loads<0>();
+      mma(u, j + u);
+      wait_reads();
+      if (j + U + u < cnt) load(u, j + U + u);
+    }
+  }
+  j += U;
+  wait_loads<0>();
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (j + u < cnt) mma(u, j + u);
+  wait_reads();
+}
+
 // Tile index of workgroup `bid` among nx * ny tiles, XCD-aware and grouped.
 __device__ __forceinline__ void tile_of(int bid, int nx, int ny, int& tx, int& ty) {
   tile_at(xcd_order(bid, nx * ny), nx, ny, tx, ty);

@@ -207,6 +207,17 @@ constexpr int kI8DecodeCodes = 16384;
 inline bool i8_decode_fits(int64_t m, int64_t k) { return m <= 4 && m * k <= kI8DecodeCodes; }
 hipError_t launch_i8_decode(const I8Set& set, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora, hipStream_t s);
 
+// Input gradient of 1 <= count <= kGemvMaxGroup 8-bit weights of one k, summed
+// (the LoRA term only with count 1).  `part` takes i8_dx_workspace_bytes()
+// bytes for the sums of a reduction that is split over workgroups; with fewer
+// (or nullptr) it is not split.
+size_t i8_dx_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m);
+hipError_t launch_i8_dx(const WView* ws, const uint16_t* const* dys, int count, int64_t m, uint16_t* dX,
+                        const LoraDx& lora, float* part, size_t part_bytes, hipStream_t s);
+// The same by k_bwd_dx's bk x bm tiles (k_bwd.hip: 256 x 256, 256 x 128, 128 x 128).
+hipError_t launch_bwd_dx_i8_tiles(const WView* ws, const uint16_t* const* dys, int count, int bk, int bm, int64_t m,
+                                  uint16_t* dX, const LoraDx& lora, hipStream_t s);
+
 // ---- gradient norm (k_grad.hip) -------------------------------------------------
 // Tensors of one launch, in the kernel's arguments (they may take 4 KiB).
 constexpr int kGradTable = 120;

@@ -346,6 +346,18 @@ lbq_status lbq_linear_bwd_dx(const lbq_desc* desc, const lbq_qtensor* q, const u
 lbq_status lbq_linear_bwd_dx_grouped(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
                                      const uint16_t* const* dYs, int64_t m, uint16_t* dX, void* stream);
 
+/* lbq_linear_bwd_dx_grouped (count = 1: lbq_linear_bwd_dx) with a workspace.
+ * The input gradient of INT8 weights with few outputs splits the rows over
+ * several workgroups, whose fp32 sums a second kernel adds in a fixed order,
+ * when the workspace holds lbq_linear_bwd_dx_grouped_workspace_bytes(count,
+ * descs, m) bytes (16-byte aligned); with less, or NULL, it runs unsplit, as
+ * the entries without one do.  The two results agree within fp32 rounding,
+ * not bit for bit.  Other formats take none (0 bytes). */
+size_t lbq_linear_bwd_dx_grouped_workspace_bytes(int32_t count, const lbq_desc* descs, int64_t m);
+lbq_status lbq_linear_bwd_dx_grouped_ws(int32_t count, const lbq_desc* descs, const lbq_qtensor* qs,
+                                        const uint16_t* const* dYs, int64_t m, uint16_t* dX, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
 /* Workspace bytes lbq_lora_bwd needs for m rows and rank r (0 for m <= 0). */
 size_t lbq_lora_bwd_workspace_bytes(const lbq_desc* desc, int64_t m, int32_t r);
 

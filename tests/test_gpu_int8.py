@@ -374,6 +374,55 @@ def test_bwd_dx(L, n, k):
         assert (np.abs(dx - ref) <= tol).all(), np.max(np.abs(dx - ref) / tol)
 
 
+@pytest.mark.parametrize("n,k,m", [(4096, 4096, 40), (14336, 1024, 16), (6000, 256, 3), (4104, 64, 100), (1000, 8192, 520),
+                                   (512, 4096, 1100)])
+def test_bwd_dx_workspace_and_without(L, n, k, m):
+    """The reduction split over workgroups (workspace, whatever it holds), and
+    unsplit through the entry without one or with one byte less."""
+    import ctypes
+    qw, (q, s) = weight(L, 3 * n + k, n, k)
+    dy = SI.bf16_normal(m + n, (m, n), 0.01)
+    rows = np.unique(np.linspace(0, m - 1, 16).astype(int))
+    ref, tol = grad_bound([O.bf16_to_f64(dy)[rows]], [O.bf16_to_f64(I8.dequant_bf16(q, s))])
+    need = L.lbq_linear_bwd_dx_grouped_workspace_bytes([qw], m)
+    dY = to_dev_bf16(dy)
+    outs = []
+    for size in {need, max(need - 1, 0)}:
+        w = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+        for _ in range(2):
+            outs.append(L.lbq_linear_bwd_dx(dY, qw, workspace=w))
+            dx = O.bf16_to_f64(bf16_bits_host(outs[-1]))[rows]
+            assert (np.abs(dx - ref) <= tol).all()
+        assert torch.equal(outs[-1], outs[-2])
+    plain = torch.empty((m, k), dtype=torch.bfloat16, device=DEV)
+    t = qw.qtensor()
+    assert L.lib.lbq_linear_bwd_dx(ctypes.byref(qw.desc), ctypes.byref(t), dY.data_ptr(), m, plain.data_ptr(),
+                                   torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    dx = O.bf16_to_f64(bf16_bits_host(plain))[rows]
+    assert (np.abs(dx - ref) <= tol).all()
+    if need:
+        assert torch.equal(plain, outs[-1]) or torch.equal(plain, outs[1])
+    else:
+        assert torch.equal(plain, outs[0])
+
+
+@pytest.mark.parametrize("n,k,m", [(72, 128, 5), (72, 128, 200), (40, 4096, 64), (200, 2048, 2100), (72, 4096, 1100), (200, 8192, 1000)])
+def test_bwd_dx_next_token_stays_out(L, n, k, m):
+    """n % 32 != 0: a token's last slice of rows reads into the next token's
+    gradients; an infinity there spoils that token alone, on every path."""
+    qw, (q, s) = weight(L, 12, n, k)
+    dy = SI.bf16_normal(m, (m, n), 0.01)
+    w = torch.empty(L.lbq_linear_bwd_dx_grouped_workspace_bytes([qw], m), dtype=torch.uint8, device=DEV)
+    for ws in (w, w[:0]):
+        dy[3, :8] = SI.bf16_normal(1, (8,), 0.01)
+        clean = bf16_bits_host(L.lbq_linear_bwd_dx(to_dev_bf16(dy), qw, workspace=ws))
+        dy[3, :8] = 0x7F80
+        dx = bf16_bits_host(L.lbq_linear_bwd_dx(to_dev_bf16(dy), qw, workspace=ws))
+        assert np.array_equal(np.delete(dx, 3, 0), np.delete(clean, 3, 0))
+        assert not np.isfinite(O.bf16_to_f64(dx[3])).any()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_bwd_dx_grouped(L, m):
     k = 576
