@@ -365,7 +365,7 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   }
   __syncthreads();
   int buf = 0;
-  if constexpr (WGK * WGM == 8) {
+  if constexpr (WGK * WGM == 8 && BM == 256) {
     // Two phases per stage, with a barrier between them: the first four waves
     // stage the next tile while the last four run their MFMAs, then the other
     // way round.  Waves w and w + 4 share a SIMD, so at any time one of them
@@ -374,7 +374,10 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     // conversions are a chain of short instructions that would otherwise wait
     // behind the MFMA wave's issue slots, while the MFMAs queue up anyway
     // (8B NF4+DQ layer at m = 4096, against raising the MFMA wave: forward
-    // +0.8-1.5%, input gradient +1%).
+    // +0.8-1.5%, input gradient +1%).  (128 tokens: a phase's MFMAs are no
+    // longer than its staging, and the second barrier costs more than the overlap
+    // gains: the 8-bit gradient of 2048 tokens through q, k and v 144 -> 125 us
+    // with one.)
     const bool late = wave >= 4;
     auto stage = [&](int64_t t) {
       __builtin_amdgcn_s_setprio(1);

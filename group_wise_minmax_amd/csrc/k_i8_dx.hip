@@ -228,7 +228,7 @@ constexpr double kMostPart = 256e6;  // bytes of sums of a split reduction
 //  * k_i8_dx, per slice of 32 rows (a wave's eighth of it) with r workgroups a CU:
 //    0.060 + 0.080 r (tm 1), 0.065 + 0.088 r (2), 0.084 + 0.120 r (4); a split adds a
 //    second launch and the traffic of the sums.
-//  * k_bwd_dx, per 64 rows: 0.84 a round of 128 x 128 tiles and 0.1, 1.27 a round of
+//  * k_bwd_dx, per 64 rows: 0.84 a round of 128 x 128 tiles and 0.1, 1.10 a round of
 //    256 x 128, 1.78 a round of 256 x 256.
 DxChoice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
   static constexpr double kBase[3] = {2.7, 2.9, 3.5}, kSlice[3] = {0.060, 0.065, 0.084},
@@ -251,7 +251,7 @@ DxChoice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
   }
   const double stages = std::ceil(n / 64.0);
   const double t128 = 3.6 + stages * (0.84 * std::ceil(ceil_div(k, 128) * ceil_div(m, 128) / 256.0) + 0.105);
-  const double t256x128 = 5.0 + stages * 1.27 * std::ceil(ceil_div(k, 256) * ceil_div(m, 128) / 256.0);
+  const double t256x128 = 5.0 + stages * 1.10 * std::ceil(ceil_div(k, 256) * ceil_div(m, 128) / 256.0);
   const double t256 = 5.2 + stages * 1.78 * std::ceil(ceil_div(k, 256) * ceil_div(m, 256) / 256.0);
   if (t128 < least) least = t128, best = {0, 1, 0, 128, 128};
   if (t256x128 < least) least = t256x128, best = {0, 1, 0, 256, 128};

@@ -228,11 +228,17 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   }
   if constexpr (LORA) {
     // the adapter term on bf16 MFMA: B [n][r] . T [m][rp], r zero-padded to rp
+    const bool whole = (lora.r & 7) == 0 && (reinterpret_cast<uintptr_t>(lora.b) & 15) == 0;
     for (int ks = 0; ks < lora.rp; ks += 32) {
       u32x4_t bf[TN], tf[TM];
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
         const int64_t nr = n0 + (wn * TN + a) * 16 + li;
+        if (whole) {
+          bf[a] = u32x4_t{0u, 0u, 0u, 0u};
+          if (nr < n && ks + 8 * lg < lora.r) bf[a] = *reinterpret_cast<const u32x4_t*>(lora.b + nr * lora.r + ks + 8 * lg);
+          continue;
+        }
         uint32_t v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
