@@ -39,25 +39,26 @@ struct DxSet {
   int count;
 };
 
-// Columns kb .. kb + 15 of token mr from their sums, + G . A of the adapters.
-__device__ __forceinline__ void store_dx(float (&v)[16], int mr, int kb, int k, uint16_t* __restrict__ dX, const LoraDx& lora) {
+// Columns kb .. kb + 4 N - 1 of token mr from their sums, + G . A of the adapters.
+template <int N>
+__device__ __forceinline__ void store_dx(float (&v)[4 * N], int mr, int kb, int k, uint16_t* __restrict__ dX, const LoraDx& lora) {
   if (lora.g != nullptr) {
     for (int j = 0; j < lora.r; ++j) {
       const float g = __uint_as_float((uint32_t)lora.g[(int64_t)mr * lora.rp + j] << 16);
-      const u32x4_t* ar = reinterpret_cast<const u32x4_t*>(lora.a + (int64_t)j * k + kb);
+      const uint2* ar = reinterpret_cast<const uint2*>(lora.a + (int64_t)j * k + kb);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4_t a = ar[h];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[8 * h + c] = fmaf(g, (c & 1) ? bf16_hi(a[c >> 1]) : bf16_lo(a[c >> 1]), v[8 * h + c]);
+      for (int h = 0; h < N; ++h) {
+        const uint2 a = ar[h];
+        v[4 * h] = fmaf(g, bf16_lo(a.x), v[4 * h]);
+        v[4 * h + 1] = fmaf(g, bf16_hi(a.x), v[4 * h + 1]);
+        v[4 * h + 2] = fmaf(g, bf16_lo(a.y), v[4 * h + 2]);
+        v[4 * h + 3] = fmaf(g, bf16_hi(a.y), v[4 * h + 3]);
       }
     }
   }
-  u32x4_t* o = reinterpret_cast<u32x4_t*>(dX + (int64_t)mr * k + kb);
+  uint2* o = reinterpret_cast<uint2*>(dX + (int64_t)mr * k + kb);
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    o[h] = u32x4_t{cvt_pk_bf16(v[8 * h], v[8 * h + 1]), cvt_pk_bf16(v[8 * h + 2], v[8 * h + 3]),
-                   cvt_pk_bf16(v[8 * h + 4], v[8 * h + 5]), cvt_pk_bf16(v[8 * h + 6], v[8 * h + 7])};
+  for (int h = 0; h < N; ++h) o[h] = make_uint2(cvt_pk_bf16(v[4 * h], v[4 * h + 1]), cvt_pk_bf16(v[4 * h + 2], v[4 * h + 3]));
 }
 
 // Slices [per * blockIdx.y, + per) of the reduction.  `part`: [gridDim.y][m][k]
@@ -180,29 +181,22 @@ __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int
     for (int i = 0; i < 4; ++i) o[i] = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
     return;
   }
-  store_dx(v, mr, kb, k, dX, lora);
+  store_dx<4>(v, mr, kb, k, dX, lora);
 }
 
-// dX from the sums of ks ranges: one thread for 16 columns of a token.
+// dX from the sums of ks ranges: one thread for four columns of a token.
 __global__ __launch_bounds__(256) void k_i8_dx_reduce(const float* __restrict__ part, int ks, int m, int k,
                                                      uint16_t* __restrict__ dX, LoraDx lora) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = k / 16;
+  const int per = k / 4;
   if (i >= (int64_t)m * per) return;
-  const int mr = (int)(i / per), kb = 16 * (int)(i % per);
-  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(part + (int64_t)mr * k + kb);
-  f32x4_t r[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) r[h] = p[h];
-  for (int j = 1; j < ks; ++j) {
-    p += (int64_t)m * k / 4;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) r[h] += p[h];
-  }
-  float v[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) v[c] = r[c >> 2][c & 3];
-  store_dx(v, mr, kb, k, dX, lora);
+  const int64_t stride = (int64_t)m * per;
+  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(part) + i;
+  f32x4_t r = p[0];
+#pragma unroll 3
+  for (int j = 1; j < ks; ++j) r += p[j * stride];
+  float v[4] = {r[0], r[1], r[2], r[3]};
+  store_dx<1>(v, (int)(i / per), 4 * (int)(i % per), k, dX, lora);
 }
 
 template <int TM, int U>
@@ -292,7 +286,7 @@ hipError_t launch_i8_dx(const WView* ws, const uint16_t* const* dys, int count, 
   else if (c.tm == 2) launch<2, 3>(set, m, k, c.ks, c.per, dX, part, lora, s);
   else launch<4, 3>(set, m, k, c.ks, c.per, dX, part, lora, s);
   if (part != nullptr)
-    hipLaunchKernelGGL(k_i8_dx_reduce, dim3((unsigned)((m * (k / 16) + 255) / 256)), dim3(256), 0, s, part, c.ks, (int)m,
+    hipLaunchKernelGGL(k_i8_dx_reduce, dim3((unsigned)((m * (k / 4) + 255) / 256)), dim3(256), 0, s, part, c.ks, (int)m,
                        (int)k, dX, lora);
   return hipGetLastError();
 }
