@@ -17,6 +17,8 @@
 
 #include "lbq_device.h"
 
+#include <algorithm>
+
 namespace lbq {
 
 namespace {
@@ -101,9 +103,14 @@ __global__ __launch_bounds__(NT) void k_i8_quant_rows(const T* __restrict__ X, i
   }
 }
 
+// Rows of one launch: a grid has fewer than 2^32 threads, and a row up to 1024.
+constexpr int64_t kMostRows = int64_t(1) << 21;
+
 template <int NT, int NC, bool KEEP, typename T>
 hipError_t launch_rows(const T* X, int64_t rows, int64_t k, int64_t ldx, int8_t* Q, float* scales, hipStream_t s) {
-  hipLaunchKernelGGL((k_i8_quant_rows<T, NT, NC, KEEP>), dim3((unsigned)rows), dim3(NT), 0, s, X, ldx, k, Q, scales);
+  for (int64_t r = 0; r < rows; r += kMostRows)
+    hipLaunchKernelGGL((k_i8_quant_rows<T, NT, NC, KEEP>), dim3((unsigned)std::min(rows - r, kMostRows)), dim3(NT), 0, s,
+                       X + r * ldx, ldx, k, Q + r * k, scales + r);
   return hipGetLastError();
 }
 
@@ -151,8 +158,9 @@ hipError_t launch_i8_quant_bf16(const uint16_t* X, int64_t m, int64_t k, int64_t
 }
 
 hipError_t launch_i8_dequant(const WView& w, uint16_t* out, hipStream_t s) {
-  hipLaunchKernelGGL(k_i8_dequant, dim3((unsigned)w.n), dim3(kThreads), 0, s,
-                     reinterpret_cast<const int8_t*>(w.packed), w.scales, (int)w.k, out);
+  for (int64_t r = 0; r < w.n; r += kMostRows)
+    hipLaunchKernelGGL(k_i8_dequant, dim3((unsigned)std::min(w.n - r, kMostRows)), dim3(kThreads), 0, s,
+                       reinterpret_cast<const int8_t*>(w.packed) + r * w.k, w.scales + r, (int)w.k, out + r * w.k);
   return hipGetLastError();
 }
 

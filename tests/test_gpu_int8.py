@@ -563,3 +563,24 @@ def test_backward_captured_beside_an_eager_graph(L, m):
         assert torch.equal(out, want)
     alive.float().sum().backward()
     assert torch.isfinite(x.grad).all()
+
+
+# ---------------------------------------------------------------- the largest
+
+def test_more_rows_than_a_grid_has(L):
+    """Rows of 64 beyond 2^32 threads of a workgroup a row: tokens, weights and
+    the dequantized weight repeat a small block's."""
+    block, times = 64, 2 ** 18 + 1
+    x = tokens(71, block, 64)
+    q, s = I8.tokens(x)
+    codes, scales = L.lbq_quantize_tokens(to_dev_bf16(x).repeat(times, 1))
+    q, s = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
+    assert (codes.view(times, block, 64) == q).all() and (scales.view(times, block) == s).all()
+    del codes, scales
+    W = SI.gaussian_weights(72, block, 64, outlier_seed=73)
+    q, s = I8.quantize_rows(W)
+    qw = L.lbq_quantize(to_dev_f32(W).repeat(times, 1), "int8")
+    dq = torch.from_numpy(I8.dequant_bf16(q, s).view(np.int16)).to(DEV)
+    q, s = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
+    assert (qw.packed.view(torch.int8).view(times, block, 64) == q).all() and (qw.scales.view(times, block) == s).all()
+    assert (L.lbq_dequant(qw).view(torch.int16).view(times, block, 64) == dq).all()
