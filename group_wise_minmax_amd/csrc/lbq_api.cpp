@@ -887,6 +887,22 @@ static bool grads_overlap(int32_t count, const lbq_grad* g) {
   return false;
 }
 
+// Whether the norm or the workspace, which are written, lie in a tensor of the
+// call (with `write`, in an output) or in each other.
+static bool grads_hit(int32_t count, const lbq_grad* g, bool write, const float* norm, const void* ws, size_t ws_bytes) {
+  const auto hit = [](const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+  };
+  if (hit(norm, sizeof(float), ws, ws_bytes)) return true;
+  for (int32_t i = 0; i < count; ++i) {
+    const size_t bytes = (size_t)g[i].numel * (g[i].dtype == LBQ_F32 ? 4 : 2);
+    if (hit(g[i].grad, bytes, norm, sizeof(float)) || hit(g[i].grad, bytes, ws, ws_bytes)) return true;
+    if (write && (hit(g[i].out, bytes, norm, sizeof(float)) || hit(g[i].out, bytes, ws, ws_bytes))) return true;
+  }
+  return false;
+}
+
 size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads) {
   if (check_grads(count, grads, false) != LBQ_OK) return 0;
   return align16((size_t)lbq::grad_parts(grads, count) * sizeof(double));
@@ -915,6 +931,8 @@ static lbq_status grad_body(int32_t count, const lbq_grad* grads, int32_t norm_t
       return fail(LBQ_E_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws_bytes);
     if (!aligned(workspace, 16)) return fail(LBQ_E_ALIGN, "workspace must be 16-byte aligned");
   }
+  if (grads_hit(count, grads, max_norm != nullptr, norm, workspace, need))
+    return fail(LBQ_E_SHAPE, "the norm and the workspace must lie outside the tensors and each other");
   const bool inf = norm_type == LBQ_NORM_INF;
   double* part = static_cast<double*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -423,7 +423,8 @@ size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads);
  * (device).  `out` is not looked at.  Summed in a fixed order (run-to-run
  * identical for the same sizes and alignments).  `workspace`:
  * lbq_grad_workspace_bytes(count, grads) bytes, 16-byte aligned; every launch
- * that overlaps another needs one of its own. */
+ * that overlaps another needs one of its own.  `norm` and `workspace` lie
+ * outside the tensors and each other (LBQ_E_SHAPE otherwise). */
 lbq_status lbq_grad_norm(int32_t count, const lbq_grad* grads, int32_t norm_type, float* norm, void* workspace,
                          size_t ws_bytes, void* stream);
 

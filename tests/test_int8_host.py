@@ -255,6 +255,21 @@ def test_norm_refusals_and_workspace(L):
     assert L.lib.lbq_grad_workspace_bytes(1, grads_of(L, (None, None, 0, 0))) == 0
 
 
+@pytest.mark.parametrize("norm,ws,clip", [
+    (A + 8, A + (1 << 20), False), (A + 396, A + (1 << 20), True),  # the norm in a gradient, at its end
+    (A + 8192, A + (1 << 20), True),                                # in an output
+    (A + (1 << 20), A + 4096, False), (A + (1 << 20), A + 8192 + 192, True),  # the workspace over a gradient, an output
+    (A + (1 << 20) + 12, A + (1 << 20), False),                     # one in the other
+])
+def test_norm_and_workspace_stay_outside_the_tensors(L, norm, ws, clip):
+    t = grads_of(L, *OK)
+    if clip:
+        rc = L.lib.lbq_clip_grads(2, t, 0, 1.0, norm, ws, 1 << 10, None)
+    else:
+        rc = L.lib.lbq_grad_norm(2, t, 0, norm, ws, 1 << 10, None)
+    assert status(L, rc) == "LBQ_E_SHAPE"
+
+
 def test_python_refusals_without_a_device(L):
     import torch
     with pytest.raises(ValueError):
