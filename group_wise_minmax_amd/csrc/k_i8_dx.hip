@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int
   // The weight that the loads are in; a wave's slices come in order.
   int wi = 0, n = set.n[0], begin = 0, end = set.end[0];
   __amdgpu_buffer_rsrc_t rw, rs, rd;
-  int od[TM];
+  int od[TM];  // (of up to 32 bits)
   // Loads of 16 x 64 bytes.  W: the row q + 8 g of a slice lies in slot 4 q + g, so
   // that the four rows that a read takes together are in different banks.  dY: 32
   // gradients of a token a row, in the order of i8_key.
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int
     rd = make_rsrc(set.dy[wi], (int64_t)m * n * 2);
 #pragma unroll
     for (int b = 0; b < TM; ++b)
-      od[b] = min(m0 + 16 * b + slot, m - 1) * n * 2 + 16 * ((lane & 3) ^ i8_key(slot));
+      od[b] = (int)((uint32_t)min(m0 + 16 * b + slot, m - 1) * (uint32_t)n * 2u) + 16 * ((lane & 3) ^ i8_key(slot));
   };
   bind();
   f32x4_t s[U][2];  // scales of this lane's 8 rows

@@ -380,17 +380,21 @@ struct I8Choice {
 // them on 170 products (m 1 to 3000, n 256 to 20000, k 256 to 28672, weights
 // not in cache): on these the choice is 7% off the best one on average.
 //  * k_i8_skinny: a workgroup takes 0.0125 us for a KiB of operands, and with r
-//    workgroups a CU these share its L1: 0.019 us a KiB and workgroup.
+//    workgroups a CU these share its L1: 0.019 us a KiB and workgroup.  (Its tokens
+//    are the grid's second dimension, which has 65535 workgroups.)
 //  * k_i8_gemm: a round of 256 x 256 tiles (one a CU) takes 0.8 us for 64 of k; a
 //    last round that would leave half of the chip idle is cut into 128 x 256
 //    pieces (0.26 us), one that would leave three quarters idle into 128 x 128
 //    pieces (0.204 us).  Where nothing is whole and the pieces leave CUs idle, K
 //    may be split: the integer sums cost a second launch and 0.86 us for a MB.
+constexpr int64_t kMostGridY = 65535;
+
 I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
   I8Choice best{1, {}};
   double least = 1e30;
   for (int t = 1; t <= 4; t *= 2) {
     int64_t groups = 0;
+    if (ceil_div(m, 16 * t) > kMostGridY) continue;
     for (int i = 0; i < count; ++i) groups += ceil_div(ns[i], 16 * t);
     groups *= ceil_div(m, 16 * t);
     const double r = (double)groups / 256, kib = 2.0 * t * 16 * k / 1024;

@@ -584,3 +584,29 @@ def test_more_rows_than_a_grid_has(L):
     q, s = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
     assert (qw.packed.view(torch.int8).view(times, block, 64) == q).all() and (qw.scales.view(times, block) == s).all()
     assert (L.lbq_dequant(qw).view(torch.int16).view(times, block, 64) == dq).all()
+
+
+def test_more_tokens_than_a_grid_dimension_has_tiles(L):
+    """4.2 M tokens of 64 through 8 channels: more than 65535 tiles of 64 tokens."""
+    block, times, n = 64, 2 ** 16 + 3, 8
+    x = tokens(74, block, 64)
+    qw, (q, s) = weight(L, 75, n, 64)
+    y = L.lbq_linear_fwd(to_dev_bf16(x).repeat(times, 1), qw)
+    xq, xs = I8.tokens(x)
+    want = torch.from_numpy(I8.product_bf16(xq, xs, q, s).view(np.int16)).to(DEV)
+    assert (y.view(torch.int16).view(times, block, n) == want).all()
+
+
+def test_gradient_beyond_31_bits_of_bytes(L):
+    """4.26 GB of output gradients: the last tokens against the formula in 64 bits."""
+    m, n, k = 65000, 32768, 64
+    g = torch.Generator(device=DEV).manual_seed(76)
+    dY = torch.randn(m, n, generator=g, device=DEV, dtype=torch.bfloat16)
+    qw, (q, s) = weight(L, 77, n, k)
+    dx = L.lbq_linear_bwd_dx(dY, qw)
+    w = L.lbq_dequant(qw).double()
+    for rows in (slice(0, 40), slice(32700, 32800), slice(m - 70, m)):
+        d = dY[rows].double()
+        want, size = d @ w, d.abs() @ w.abs()
+        err = (dx[rows].double() - want).abs()
+        assert (err <= HALF * want.abs() + (1 + HALF) * (n + 2) * E32 * size).all()
