@@ -121,6 +121,14 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need_out(out: torch.Tensor, m: int, qw: "QuantizedWeight", name: str = "out") -> None:
+    """A forward's output: m rows, and a column for every channel unless out_rows places them."""
+    if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
+        raise ValueError(f"{name} must be bf16 [m, >=n] with unit column stride")
+    if qw.out_rows is None and out.shape[1] < qw.n:
+        raise ValueError(f"{name} must have at least {qw.n} columns")
+
+
 @dataclass
 class QuantizedWeight:
     """Device buffers of one quantized weight plus its descriptor."""
@@ -287,8 +295,7 @@ def lbq_linear_fwd(X: torch.Tensor, qw: QuantizedWeight, out: Optional[torch.Ten
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
         out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
-    if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
-        raise ValueError("out must be bf16 [m, >=n] with unit column stride")
+    _need_out(out, m, qw)
     nbytes = lbq_linear_workspace_bytes(qw, m)
     if workspace is None:
         workspace = _ws(nbytes, X.device)
@@ -312,8 +319,7 @@ def lbq_linear_fwd_noalloc(X: torch.Tensor, qw: QuantizedWeight, out: Optional[t
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
         out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
-    if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
-        raise ValueError("out must be bf16 [m, >=n] with unit column stride")
+    _need_out(out, m, qw)
     q = qw.qtensor()
     _same_device(X.device, qw.packed, out)
     with _on(X.device):
@@ -348,9 +354,7 @@ def lbq_linear_fwd_grouped(X: torch.Tensor, qws, outs=None, workspace: Optional[
             if q.out_rows is not None:
                 raise ValueError(f"outs[{i}] must be given when out_rows is set")
             outs[i] = torch.empty((m, q.n), dtype=torch.bfloat16, device=X.device)
-        o = outs[i]
-        if o.dtype != torch.bfloat16 or o.dim() != 2 or o.shape[0] != m or o.stride(1) != 1:
-            raise ValueError(f"outs[{i}] must be bf16 [m, >=n] with unit column stride")
+        _need_out(outs[i], m, q, f"outs[{i}]")
     descs = (Desc * count)(*[q.desc for q in qws])
     qts = (QTensor * count)(*[q.qtensor() for q in qws])
     ys = (ctypes.c_void_p * count)(*[o.data_ptr() for o in outs])
@@ -432,12 +436,15 @@ def lbq_lora_fwd(X: torch.Tensor, qw: QuantizedWeight, A: torch.Tensor, B: torch
     _need(B, "B", torch.bfloat16)
     m = X.shape[0]
     r = A.shape[0]
+    if X.dim() != 2 or X.shape[1] != qw.k:
+        raise ValueError(f"X must be [m, {qw.k}]")
     if A.shape[1] != qw.k or B.shape != (qw.n, r):
         raise ValueError("A must be [r, k] and B [n, r]")
     if out is None:
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
         out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
+    _need_out(out, m, qw)
     nbytes = lbq_lora_workspace_bytes(qw, m, r)
     if workspace is None:
         workspace = _ws(nbytes, X.device)
@@ -576,10 +583,7 @@ def lbq_linear_fwd_tokens(codes: torch.Tensor, scales: torch.Tensor, qw: Quantiz
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
         out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=dev)
-    if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != m or out.stride(1) != 1:
-        raise ValueError("out must be bf16 [m, >=n] with unit column stride")
-    if qw.out_rows is None and out.shape[1] < qw.n:
-        raise ValueError(f"out must have at least {qw.n} columns")
+    _need_out(out, m, qw)
     _same_device(dev, scales, out, qw.packed, workspace)
     if workspace is None:
         workspace = _ws(lib.lbq_linear_fwd_tokens_workspace_bytes(ctypes.byref(qw.desc), m), dev)

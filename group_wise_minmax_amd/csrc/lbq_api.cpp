@@ -264,9 +264,13 @@ size_t align16(size_t b) { return (b + 15) / 16 * 16; }
 // Workspace of the forward of INT8 weights that share X (16-byte aligned
 // pieces): the tokens' codes [m][k] and scales [m], then what the product
 // takes; none where one launch quantizes and multiplies.
+// (0 as well for sizes that the calls refuse)
+bool i8_rows_fit(int64_t m, int64_t k) {
+  return m >= 1 && m < (int64_t(1) << 31) && (uint64_t)(m + 256) * (uint64_t)k * 2 < (uint64_t(1) << 32);
+}
 size_t i8_token_bytes(int64_t m, int64_t k) { return align16((size_t)m * (size_t)k) + align16((size_t)m * sizeof(float)); }
 size_t i8_workspace(const int64_t* ns, int count, int64_t k, int64_t m) {
-  if (lbq::i8_decode_fits(m, k)) return 0;
+  if (!i8_rows_fit(m, k) || lbq::i8_decode_fits(m, k)) return 0;
   return i8_token_bytes(m, k) + lbq::i8_fwd_workspace_bytes(ns, count, k, m);
 }
 hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* rows, int count,
@@ -449,7 +453,7 @@ lbq_status lbq_quantize_tokens(const uint16_t* X, int64_t m, int64_t k, int64_t 
 }
 
 size_t lbq_linear_fwd_tokens_workspace_bytes(const lbq_desc* desc, int64_t m) {
-  if (check_desc(desc) != LBQ_OK || desc->format != LBQ_INT8 || m < 1) return 0;
+  if (check_desc(desc) != LBQ_OK || desc->format != LBQ_INT8 || !i8_rows_fit(m, desc->k)) return 0;
   return lbq::i8_fwd_workspace_bytes(&desc->n, 1, desc->k, m);
 }
 
@@ -681,6 +685,7 @@ size_t lbq_linear_bwd_dx_grouped_workspace_bytes(int32_t count, const lbq_desc* 
     if (check_desc(&descs[i]) != LBQ_OK || descs[i].k != descs[0].k || descs[i].format != LBQ_INT8) return 0;
     ns[i] = descs[i].n;
   }
+  if (!i8_rows_fit(m, descs[0].k)) return 0;
   return lbq::i8_dx_workspace_bytes(ns, count, descs[0].k, m);
 }
 
@@ -729,7 +734,7 @@ size_t lbq_lora_bwd_workspace_bytes(const lbq_desc* desc, int64_t m, int32_t r) 
   size_t part = std::max(lbq::lora_xa_part_bytes(m, desc->n, r) + lbq::lora_xa_part_bytes(m, desc->k, r),
                          lbq::lora_outer_part_bytes(m, desc->k, r) + lbq::lora_outer_part_bytes(m, desc->n, r));
   // between them the input gradient, whose reduction may be split (INT8)
-  if (desc->format == LBQ_INT8) part = std::max(part, lbq::i8_dx_workspace_bytes(&desc->n, 1, desc->k, m));
+  if (desc->format == LBQ_INT8 && i8_rows_fit(m, desc->k)) part = std::max(part, lbq::i8_dx_workspace_bytes(&desc->n, 1, desc->k, m));
   return align16(rp * (size_t)desc->n * 2) + align16((size_t)m * rp * 2) + 2 * align16(rp * mp * 2) + align16(part);
 }
 

@@ -352,6 +352,20 @@ def test_refused_tensors(L):
         L.lbq_quantize(torch.zeros((64, 256), device=DEV), "int8", out=L.lbq_quantize(torch.zeros((64, 256), device=DEV)))
 
 
+def test_refused_outputs(L):
+    qw, _ = weight(L, 62, 64, 256)
+    X = torch.zeros((3, 256), dtype=torch.bfloat16, device=DEV)
+    A, B = X[:2].contiguous(), torch.zeros((64, 2), dtype=torch.bfloat16, device=DEV)
+    wide = torch.empty((3, 100), dtype=torch.bfloat16, device=DEV)
+    for out in (wide[:, :63], wide[:2, :64], wide[:, :64].float(), wide.t()[:64].t()[:, ::2]):
+        for call in (lambda: L.lbq_linear_fwd(X, qw, out=out), lambda: L.lbq_linear_fwd_noalloc(X, qw, out=out),
+                     lambda: L.lbq_linear_fwd_grouped(X, [qw], [out]), lambda: L.lbq_lora_fwd(X, qw, A, B, 1.0, out=out)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        L.lbq_lora_fwd(X[:, :128].contiguous(), qw, A, B, 1.0)
+
+
 # ------------------------------------------------------------------ input gradient
 
 def grad_bound(dys, whats):

@@ -255,6 +255,30 @@ def test_norm_refusals_and_workspace(L):
     assert L.lib.lbq_grad_workspace_bytes(1, grads_of(L, (None, None, 0, 0))) == 0
 
 
+def test_sizes_that_are_refused_take_no_workspace(L):
+    d = L.make_desc("int8", 64, 256)
+    for m in ((1 << 23) - 256, 1 << 31, (1 << 63) - 1):
+        assert L.lib.lbq_linear_workspace_bytes(ctypes.byref(d), m) == 0
+        assert L.lib.lbq_linear_fwd_tokens_workspace_bytes(ctypes.byref(d), m) == 0
+        assert L.lib.lbq_linear_bwd_dx_grouped_workspace_bytes(1, ctypes.byref(d), m) == 0
+    assert L.lib.lbq_linear_workspace_bytes(ctypes.byref(d), (1 << 23) - 257) >= ((1 << 23) - 257) * 260
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(count=0), "LBQ_E_SHAPE"), (dict(count=9), "LBQ_E_SHAPE"), (dict(other="minmax"), "LBQ_E_UNSUPPORTED"),
+    (dict(other_k=512), "LBQ_E_SHAPE"), (dict(ws=FAKE + 8), "LBQ_E_ALIGN"), (dict(dY=None), "LBQ_E_NULL"),
+    (dict(m=-1), "LBQ_E_SHAPE"), (dict(m=(1 << 23) - 256), "LBQ_E_SHAPE"), (dict(dX=FAKE + 8), "LBQ_E_ALIGN"),
+])
+def test_bwd_dx_grouped_ws_refusals(L, kw, code):
+    a = dict(count=2, other="int8", other_k=256, ws=FAKE, dY=FAKE, m=40, dX=FAKE)
+    a.update(kw)
+    descs = (L.Desc * 2)(L.make_desc("int8", 64, 256), L.make_desc(a["other"], 64, a["other_k"]))
+    qts = (L.QTensor * 2)(q_of(L), q_of(L, zeros=FAKE))
+    dys = (ctypes.c_void_p * 2)(FAKE, a["dY"])
+    rc = L.lib.lbq_linear_bwd_dx_grouped_ws(a["count"], descs, qts, dys, a["m"], a["dX"], a["ws"], 1 << 30, None)
+    assert status(L, rc) == code
+
+
 @pytest.mark.parametrize("norm,ws,clip", [
     (A + 8, A + (1 << 20), False), (A + 396, A + (1 << 20), True),  # the norm in a gradient, at its end
     (A + 8192, A + (1 << 20), True),                                # in an output
