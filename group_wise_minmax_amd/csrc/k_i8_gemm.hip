@@ -24,6 +24,9 @@ struct I8Stage {
 
 constexpr int I8K = 64;
 
+// Channels of a token's partial sums: 16 bytes at a time for any n.
+__host__ __device__ constexpr int padded(int n) { return (n + 3) & ~3; }
+
 // Order of a half step's instructions: R LDS reads and L loads, one after each
 // MFMA, then the rest of the M MFMAs.
 template <int R, int L, int M>
@@ -56,7 +59,7 @@ constexpr int i8_slices() {
 
 // The BN x BM outputs from channel n0 of weight wi and token m0 on, by WGN x
 // WGM waves, summed over `slices` slices of K from s0 on.  With PART the integer
-// sums go to part, [m][n], where that is not null.
+// sums go to part, [m][padded(n)], where that is not null.
 template <int BN, int BM, int WGN, int WGM, bool LORA, bool PART>
 __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restrict__ Xq, const float* __restrict__ xs,
                                         int m, int k, const LoraEpi& lora, int wi, int n0, int m0, int s0, int slices,
@@ -190,22 +193,16 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
 
   // Epilogue: lane l holds channels n = 4 (l / 16) + i of token m = l % 16.
   if (PART && part != nullptr) {
-    const bool vec = (n & 3) == 0;
+    const int n4 = padded(n);
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
       const int mr = m0 + (wm * TM + b) * 16 + li;
       if (mr >= m) continue;
-      int* prow = part + (int64_t)mr * n;
+      int* prow = part + (int64_t)mr * n4;
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
         const int nb = n0 + (wn * TN + a) * 16 + 4 * lg;
-        if (vec && nb < n) {
-          *reinterpret_cast<i32x4_t*>(prow + nb) = acc[a][b];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (nb + i < n) prow[nb + i] = acc[a][b][i];
-        }
+        if (nb < n4) *reinterpret_cast<i32x4_t*>(prow + nb) = acc[a][b];
       }
     }
     return;
@@ -228,33 +225,13 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   }
   if constexpr (LORA) {
     // the adapter term on bf16 MFMA: B [n][r] . T [m][rp], r zero-padded to rp
-    const bool whole = (lora.r & 7) == 0 && (reinterpret_cast<uintptr_t>(lora.b) & 15) == 0;
+    const bool whole = lora_whole(lora);
     for (int ks = 0; ks < lora.rp; ks += 32) {
       u32x4_t bf[TN], tf[TM];
 #pragma unroll
-      for (int a = 0; a < TN; ++a) {
-        const int64_t nr = n0 + (wn * TN + a) * 16 + li;
-        if (whole) {
-          bf[a] = u32x4_t{0u, 0u, 0u, 0u};
-          if (nr < n && ks + 8 * lg < lora.r) bf[a] = *reinterpret_cast<const u32x4_t*>(lora.b + nr * lora.r + ks + 8 * lg);
-          continue;
-        }
-        uint32_t v[4];
+      for (int a = 0; a < TN; ++a) bf[a] = lora_b(lora, whole, n0 + (wn * TN + a) * 16 + li, n, ks + 8 * lg);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c0 = ks + 8 * lg + 2 * j;
-          uint32_t lo = 0, hi = 0;
-          if (nr < n && c0 < lora.r) lo = lora.b[nr * lora.r + c0];
-          if (nr < n && c0 + 1 < lora.r) hi = lora.b[nr * lora.r + c0 + 1];
-          v[j] = lo | (hi << 16);
-        }
-        bf[a] = u32x4_t{v[0], v[1], v[2], v[3]};
-      }
-#pragma unroll
-      for (int b = 0; b < TM; ++b) {
-        const int64_t mr = m0 + (wm * TM + b) * 16 + li;
-        tf[b] = mr < m ? *reinterpret_cast<const u32x4_t*>(lora.t + mr * lora.rp + ks + 8 * lg) : u32x4_t{0u, 0u, 0u, 0u};
-      }
+      for (int b = 0; b < TM; ++b) tf[b] = lora_t(lora, m0 + (wm * TM + b) * 16 + li, m, ks + 8 * lg);
 #pragma unroll
       for (int a = 0; a < TN; ++a)
 #pragma unroll
@@ -341,30 +318,23 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan p
   else i8_tile<128, 128, 2, 4, LORA, !LORA>(set, Xq, xs, m, k, lora, wi, n0, m0, s0, steps, part, lds);
 }
 
-// Outputs from the integer sums of ks K ranges: one thread for four channels of
-// a token.
+// Outputs from the integer sums of ks K ranges: 16 channels of 16 tokens a wave.
 __global__ __launch_bounds__(256) void k_i8_reduce(I8Set set, const int* __restrict__ part, int ks,
                                                   const float* __restrict__ xs, int m, LoraEpi lora) {
   const int wi = blockIdx.z;
   const int n = set.n[wi];
-  const int nb = 4 * (blockIdx.x * 256 + threadIdx.x), mr = blockIdx.y;
-  if (nb >= n) return;
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int n0 = 64 * blockIdx.x + 16 * (threadIdx.x >> 6), nb = n0 + 4 * lg;
+  const int mr = 16 * blockIdx.y + li;
+  if (n0 >= n) return;
   const int64_t stride = (int64_t)m * set.n_end[set.count - 1];
-  const int* p = part + (int64_t)m * (wi == 0 ? 0 : set.n_end[wi - 1]) + (int64_t)mr * n + nb;
-  int acc[4] = {0, 0, 0, 0};
-  if ((n & 3) == 0) {
-    i32x4_t v = {0, 0, 0, 0};
+  const int* p = part + (int64_t)m * (wi == 0 ? 0 : set.n_end[wi - 1]) + (int64_t)mr * padded(n) + nb;
+  i32x4_t v = {0, 0, 0, 0};
+  if (mr < m && nb < n) {
 #pragma unroll 4
     for (int j = 0; j < ks; ++j) v += *reinterpret_cast<const i32x4_t*>(p + j * stride);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = v[i];
-  } else {
-    for (int j = 0; j < ks; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (nb + i < n) acc[i] += p[j * stride + i];
   }
-  i8_store(set, wi, xs[mr], acc, mr, nb, lora);
+  i8_store(set, wi, mr < m ? xs[mr] : 0.f, v, mr, m, n0, lora);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -433,7 +403,7 @@ size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m
   const I8Choice c = choose(ns, count, k, m);
   if (c.skinny != 0 || c.plan.ks == 1) return 0;
   int64_t n = 0;
-  for (int i = 0; i < count; ++i) n += ns[i];
+  for (int i = 0; i < count; ++i) n += padded((int)ns[i]);
   return (size_t)c.plan.ks * (size_t)m * (size_t)n * sizeof(int);
 }
 
@@ -448,7 +418,7 @@ I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const in
     set.rows[i] = out_rows[i];
     set.ldy[i] = ldys[i];
     set.n[i] = (int)ws[i].n;
-    n += ws[i].n;
+    n += padded((int)ws[i].n);
     set.n_end[i] = n;
   }
   return set;
@@ -475,7 +445,7 @@ hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs
   else
     hipLaunchKernelGGL(k_i8_gemm<false>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, (int)k, lora, part);
   if (part != nullptr)
-    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)ceil_div(most, 1024), (unsigned)m, (unsigned)set.count), dim3(256), 0, s,
+    hipLaunchKernelGGL(k_i8_reduce, dim3((unsigned)ceil_div(most, 64), (unsigned)ceil_div(m, 16), (unsigned)set.count), dim3(256), 0, s,
                        set, part, plan.ks, xs, (int)m, lora);
   return hipGetLastError();
 }

@@ -119,9 +119,8 @@ __global__ __launch_bounds__(kThreads) void k_i8_skinny(I8Set set, const int8_t*
     i32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const i32x4_t*>(&ring[w][0][0])[blk * 64 + lane];
-    const int mr = m0 + (blk % T) * 16 + li, nb = n0 + (blk / T) * 16 + 4 * lg;
-    const int s[4] = {v[0], v[1], v[2], v[3]};
-    if (mr < m && nb < n) i8_store(set, wi, xs[mr], s, mr, nb, lora);
+    const int mr = m0 + (blk % T) * 16 + li;
+    i8_store(set, wi, mr < m ? xs[mr] : 0.f, v, mr, m, n0 + (blk / T) * 16, lora);
   }
 }
 
@@ -192,12 +191,11 @@ __global__ __launch_bounds__(kThreads) void k_i8_decode(I8Set set, const uint16_
   });
   reinterpret_cast<i32x4_t*>(&ring[wave][0][0])[lane] = acc;
   __syncthreads();
-  if (wave == 0 && li < m && n0 + 4 * lg < n) {
+  if (wave == 0) {
     i32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const i32x4_t*>(&ring[w][0][0])[lane];
-    const int sum[4] = {v[0], v[1], v[2], v[3]};
-    i8_store(set, wi, i8_scale(top_of(li), finite), sum, li, n0 + 4 * lg, lora);
+    i8_store(set, wi, i8_scale(top_of(li), finite), v, li, m, n0, lora);
   }
 }
 

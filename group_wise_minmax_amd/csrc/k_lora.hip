@@ -140,21 +140,6 @@ __global__ __launch_bounds__(256) void k_lora_xa(XaJob j0, XaJob j1, int m, int 
     }
 }
 
-// Sum of part[s * stride + off] over s < splits, in order; four loads are in
-// flight at a time.
-__device__ __forceinline__ float sum_splits(const float* __restrict__ part, int splits, int64_t stride,
-                                            int64_t off) {
-  float v = 0.f;
-  int s = 0;
-  for (; s + 4 <= splits; s += 4) {
-    const float p0 = part[(s + 0) * stride + off], p1 = part[(s + 1) * stride + off];
-    const float p2 = part[(s + 2) * stride + off], p3 = part[(s + 3) * stride + off];
-    v += p0; v += p1; v += p2; v += p3;
-  }
-  for (; s < splits; ++s) v += part[s * stride + off];
-  return v;
-}
-
 // T = bf16(sigma * sum over s of part[s][t][j]) for t < m, j < r, 0 elsewhere:
 // row-major [m][rp] into Trm and/or transposed [rp][mp] into Ttr (rows t in
 // [m, mp) zero).  A workgroup finalizes 16 rows and transposes them in LDS.
@@ -406,6 +391,15 @@ size_t lora_xa_part_bytes(int64_t m, int64_t K, int32_t r) {
   return (size_t)xa_splits(m, K) * (size_t)m * (size_t)(16 * tiles_of(r)) * sizeof(float);
 }
 
+static void launch_xa(int nt, dim3 grid, const XaJob& j0, const XaJob& j1, int64_t m, int32_t r, hipStream_t s) {
+  switch (nt) {
+    case 1: hipLaunchKernelGGL(k_lora_xa<1>, grid, dim3(256), 0, s, j0, j1, (int)m, (int)r); break;
+    case 2: hipLaunchKernelGGL(k_lora_xa<2>, grid, dim3(256), 0, s, j0, j1, (int)m, (int)r); break;
+    case 3: hipLaunchKernelGGL(k_lora_xa<3>, grid, dim3(256), 0, s, j0, j1, (int)m, (int)r); break;
+    default: hipLaunchKernelGGL(k_lora_xa<4>, grid, dim3(256), 0, s, j0, j1, (int)m, (int)r); break;
+  }
+}
+
 // One or two adapter products (count = 1 or 2; jobs[i] = X, K, A with its
 // outputs), each with its own area of fp32 partials, in one product launch and
 // one finalize launch.
@@ -427,12 +421,7 @@ hipError_t launch_lora_xa_jobs(int count, const uint16_t* const* Xs, const int64
   if (count == 1) xj[1] = xj[0], fj[1] = fj[0];
   const dim3 grid((unsigned)((m + XA_ROWS - 1) / XA_ROWS), (unsigned)sp_max, (unsigned)count);
   const int nt = tiles_of(r);
-  switch (nt) {
-    case 1: hipLaunchKernelGGL(k_lora_xa<1>, grid, dim3(256), 0, s, xj[0], xj[1], (int)m, (int)r); break;
-    case 2: hipLaunchKernelGGL(k_lora_xa<2>, grid, dim3(256), 0, s, xj[0], xj[1], (int)m, (int)r); break;
-    case 3: hipLaunchKernelGGL(k_lora_xa<3>, grid, dim3(256), 0, s, xj[0], xj[1], (int)m, (int)r); break;
-    default: hipLaunchKernelGGL(k_lora_xa<4>, grid, dim3(256), 0, s, xj[0], xj[1], (int)m, (int)r); break;
-  }
+  launch_xa(nt, grid, xj[0], xj[1], m, r, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // every job with a transposed output covers mp rows, else m
@@ -448,6 +437,15 @@ hipError_t launch_lora_xa(const uint16_t* X, int64_t m, int64_t K, const uint16_
                           int32_t rp, float sigma, float* part, uint16_t* Trm, uint16_t* Ttr,
                           int64_t mp, hipStream_t s) {
   return launch_lora_xa_jobs(1, &X, &K, &A, &Trm, &Ttr, m, r, rp, sigma, part, mp, s);
+}
+
+hipError_t launch_lora_xa_sums(const uint16_t* X, int64_t m, int64_t K, const uint16_t* A, int32_t r, int32_t rp,
+                               float sigma, float* part, uint16_t* T, XaSums* t, hipStream_t s) {
+  const int sp = xa_splits(m, K), nt = tiles_of(r);
+  const XaJob j{X, K, A, (int)((K / 32 + sp - 1) / sp), sp, part};
+  launch_xa(nt, dim3((unsigned)((m + XA_ROWS - 1) / XA_ROWS), (unsigned)sp), j, j, m, r, s);
+  *t = XaSums{part, sp, 16 * nt, r, rp, m, sigma, T};
+  return hipGetLastError();
 }
 
 size_t lora_outer_part_bytes(int64_t m, int64_t C, int32_t r) {

@@ -274,14 +274,14 @@ size_t i8_workspace(const int64_t* ns, int count, int64_t k, int64_t m) {
   return i8_token_bytes(m, k) + lbq::i8_fwd_workspace_bytes(ns, count, k, m);
 }
 hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* rows, int count,
-                  const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, void* ws, hipStream_t s) {
+                  const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, const lbq::XaSums& t, void* ws, hipStream_t s) {
   const int64_t k = w[0].k;
   const lbq::I8Set set = lbq::i8_set(w, ys, ldys, rows, count);
   if (lbq::i8_decode_fits(m, k)) return lbq::launch_i8_decode(set, X, m, k, lora, s);
   uint8_t* p = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(p);
   float* xs = reinterpret_cast<float*>(p + align16((size_t)m * (size_t)k));
-  const hipError_t e = lbq::launch_i8_quant_bf16(X, m, k, k, xq, xs, s);
+  const hipError_t e = lbq::launch_i8_quant_bf16(X, m, k, k, xq, xs, t, s);
   if (e != hipSuccess) return e;
   return lbq::launch_i8_fwd(set, xq, xs, m, k, lora, p + i8_token_bytes(m, k), s);
 }
@@ -290,7 +290,7 @@ hipError_t dispatch_fwd(const lbq_desc* desc, const lbq::WView& w, const uint16_
                         uint16_t* Y, int64_t ldy, const int32_t* out_rows,
                         const lbq::LoraEpi& lora, void* ws, size_t ws_bytes, hipStream_t s) {
   const lbq::WKind kind = kind_of(desc);
-  if (kind == lbq::WK_I8) return i8_fwd(&w, &Y, &ldy, &out_rows, 1, X, m, lora, ws, s);
+  if (kind == lbq::WK_I8) return i8_fwd(&w, &Y, &ldy, &out_rows, 1, X, m, lora, lbq::XaSums{}, ws, s);
   if (m == 1) return lbq::launch_gemv1(kind, &w, &Y, &out_rows, 1, X, lora, nf4_table(), s);
   if (use_gemvm(desc, m)) return lbq::launch_gemvm(kind, &w, &Y, &ldy, &out_rows, 1, X, m, lora, nf4_table(), s);
   if (m <= lbq::kSkinnyMaxM)
@@ -448,7 +448,7 @@ lbq_status lbq_quantize_tokens(const uint16_t* X, int64_t m, int64_t k, int64_t 
   if (X == nullptr || Xq == nullptr || xscale == nullptr) return fail(LBQ_E_NULL, "X, Xq and xscale must be non-NULL");
   if (!aligned(X, 16) || !aligned(Xq, 16)) return fail(LBQ_E_ALIGN, "X and Xq must be 16-byte aligned");
   if (!aligned(xscale, 4)) return fail(LBQ_E_ALIGN, "xscale must be 4-byte aligned");
-  return hip_status(lbq::launch_i8_quant_bf16(X, m, k, ldx, Xq, xscale, static_cast<hipStream_t>(stream)),
+  return hip_status(lbq::launch_i8_quant_bf16(X, m, k, ldx, Xq, xscale, lbq::XaSums{}, static_cast<hipStream_t>(stream)),
                     "lbq_quantize_tokens");
 }
 
@@ -652,7 +652,7 @@ lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lb
       rows[c] = qs[j].out_rows;
       ++c;
     }
-    if (kind == lbq::WK_I8) e = i8_fwd(ws, ys, lds, rows, c, X, m, none, workspace, s);
+    if (kind == lbq::WK_I8) e = i8_fwd(ws, ys, lds, rows, c, X, m, none, lbq::XaSums{}, workspace, s);
     else if (m == 1) e = lbq::launch_gemv1(kind, ws, ys, rows, c, X, none, nf4_table(), s);
     else if (gemvm) e = lbq::launch_gemvm(kind, ws, ys, lds, rows, c, X, m, none, nf4_table(), s);
     else if (m <= lbq::kSkinnyMaxM)
@@ -808,13 +808,15 @@ lbq_status lbq_lora_bwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
 
 // LoRA workspace: bf16 T = sigma X A^T [m][rp], then (16-byte aligned) fp32
 // partial sums, first of T's product and then of the small-batch kernel when
-// that kernel runs.
+// that kernel runs.  INT8: what the product takes lies behind T's partial sums.
 static size_t lora_t_bytes(int64_t m, int32_t r) {
   return ((size_t)m * (size_t)round_rank(r) * sizeof(uint16_t) + 15) / 16 * 16;
 }
 
 size_t lbq_lora_workspace_bytes(const lbq_desc* desc, int64_t m, int32_t r) {
   if (check_desc(desc) != LBQ_OK || m <= 0 || r < 1 || r > 64) return 0;
+  // INT8: the tokens' quantizer writes its codes while it reads T's partial sums
+  if (desc->format == LBQ_INT8) return lora_t_bytes(m, r) + lbq::lora_xa_part_bytes(m, desc->k, r) + fwd_workspace(desc, m, true);
   return lora_t_bytes(m, r) + std::max(lbq::lora_xa_part_bytes(m, desc->k, r), fwd_workspace(desc, m, true));
 }
 
@@ -836,10 +838,17 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
   const int32_t rp = round_rank(r);
   uint16_t* T = static_cast<uint16_t*>(workspace);
   void* part = static_cast<uint8_t*>(workspace) + lora_t_bytes(m, r);
-  hipError_t e = lbq::launch_lora_xa(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, nullptr, m, s);
-  if (e != hipSuccess) return hip_status(e, "lbq_lora_fwd (adapter product)");
   const lbq::LoraEpi lora{T, B, r, rp};
   const lbq::WView w = view_of(desc, q);
+  if (desc->format == LBQ_INT8 && !lbq::i8_decode_fits(m, desc->k)) {
+    lbq::XaSums t;
+    hipError_t e = lbq::launch_lora_xa_sums(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, &t, s);
+    if (e == hipSuccess)
+      e = i8_fwd(&w, &Y, &ldy, &q->out_rows, 1, X, m, lora, t, static_cast<uint8_t*>(part) + lbq::lora_xa_part_bytes(m, desc->k, r), s);
+    return hip_status(e, "lbq_lora_fwd");
+  }
+  const hipError_t e = lbq::launch_lora_xa(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, nullptr, m, s);
+  if (e != hipSuccess) return hip_status(e, "lbq_lora_fwd (adapter product)");
   return hip_status(dispatch_fwd(desc, w, X, m, Y, ldy, q->out_rows, lora, part, ws_bytes - lora_t_bytes(m, r), s),
                     "lbq_lora_fwd");
 }

@@ -380,6 +380,21 @@ __device__ __forceinline__ float nf4_block_scale(const WView& w, int64_t blk, fl
   }
 }
 
+// Sum of part[s * stride + off] over s < splits, in order; four loads are in
+// flight at a time.
+__device__ __forceinline__ float sum_splits(const float* __restrict__ part, int splits, int64_t stride,
+                                            int64_t off) {
+  float v = 0.f;
+  int s = 0;
+  for (; s + 4 <= splits; s += 4) {
+    const float p0 = part[(s + 0) * stride + off], p1 = part[(s + 1) * stride + off];
+    const float p2 = part[(s + 2) * stride + off], p3 = part[(s + 3) * stride + off];
+    v += p0; v += p1; v += p2; v += p3;
+  }
+  for (; s < splits; ++s) v += part[s * stride + off];
+  return v;
+}
+
 // bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
 __device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
 
@@ -442,29 +457,52 @@ __device__ __forceinline__ uint2 i8_codes_bf16(const u32x4_t& v, float s, float 
   return i8_codes([&](int i) { return (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }, s, rs, finite);
 }
 
-// Outputs of channels nb .. nb + 3 (nb < n) of weight wi and token mr from their
-// integer sums: scaled (one rounding to fp32 each: the caller's file has
-// contraction off), the adapter term T[mr] . B[channel] added in fp32.
-__device__ __forceinline__ void i8_store(const I8Set& set, int wi, float sx, const int acc[4], int64_t mr, int nb,
+// Operands of the adapter term T [m][rp] . B [n][r]^T on bf16 MFMA, c .. c + 7 of
+// the rank: of channel nr (zeros from r on and past n), and of a token (rp holds
+// zeros from r on).  `whole`: B's rows can be read 16 bytes at a time.
+__device__ __forceinline__ bool lora_whole(const LoraEpi& lora) {
+  return (lora.r & 7) == 0 && (reinterpret_cast<uintptr_t>(lora.b) & 15) == 0;
+}
+__device__ __forceinline__ u32x4_t lora_b(const LoraEpi& lora, bool whole, int64_t nr, int n, int c) {
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (whole) {
+    if (nr < n && c < lora.r) v = *reinterpret_cast<const u32x4_t*>(lora.b + nr * lora.r + c);
+    return v;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t lo = 0, hi = 0;
+    if (nr < n && c + 2 * j < lora.r) lo = lora.b[nr * lora.r + c + 2 * j];
+    if (nr < n && c + 2 * j + 1 < lora.r) hi = lora.b[nr * lora.r + c + 2 * j + 1];
+    v[j] = lo | (hi << 16);
+  }
+  return v;
+}
+__device__ __forceinline__ u32x4_t lora_t(const LoraEpi& lora, int64_t mr, int m, int c) {
+  return mr < m ? *reinterpret_cast<const u32x4_t*>(lora.t + mr * lora.rp + c) : u32x4_t{0u, 0u, 0u, 0u};
+}
+
+// Outputs of 16 channels from n0 on and 16 tokens from their integer sums, by a
+// whole wave: lane l has channels n0 + 4 (l / 16) + i of token mr, which is m0 + l %
+// 16.  Scaled (one rounding to fp32 each: the caller's file has contraction off),
+// the adapter term added on MFMA as k_i8_gemm does.  (Each lane adding its own
+// term with 2-byte loads: m = 130, n = k = 4096, rank 16 56.8 us against 28.7.)
+__device__ __forceinline__ void i8_store(const I8Set& set, int wi, float sx, const i32x4_t& acc, int64_t mr, int m, int n0,
                                          const LoraEpi& lora) {
 #pragma clang fp contract(off)
-  const int n = set.n[wi];
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int n = set.n[wi], nb = n0 + 4 * lg;
   const float* sw = set.ws[wi];
   const int32_t* rows = set.rows[wi];
-  float v[4];
+  f32x4_t v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * sx * sw[nb + i < n ? nb + i : n - 1];
   if (lora.t != nullptr) {
-    const uint16_t* t = lora.t + mr * lora.rp;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t* b = lora.b + (int64_t)(nb + i < n ? nb + i : n - 1) * lora.r;
-      float d = 0.f;
-      for (int q = 0; q < lora.r; ++q)
-        d = fmaf(__uint_as_float((uint32_t)t[q] << 16), __uint_as_float((uint32_t)b[q] << 16), d);
-      v[i] += d;
-    }
+    const bool whole = lora_whole(lora);
+    for (int ks = 0; ks < lora.rp; ks += 32)
+      v = mfma16x16x32(lora_b(lora, whole, n0 + li, n, ks + 8 * lg), lora_t(lora, mr, m, ks + 8 * lg), v);
   }
+  if (mr >= m || nb >= n) return;
   uint16_t* y = set.y[wi] + mr * set.ldy[wi];
   uint2 o;
   o.x = cvt_pk_bf16(v[0], v[1]);

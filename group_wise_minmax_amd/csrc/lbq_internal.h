@@ -153,6 +153,17 @@ size_t lora_xa_part_bytes(int64_t m, int64_t K, int32_t r);
 hipError_t launch_lora_xa(const uint16_t* X, int64_t m, int64_t K, const uint16_t* A, int32_t r,
                           int32_t rp, float sigma, float* part, uint16_t* Trm, uint16_t* Ttr,
                           int64_t mp, hipStream_t s);
+// The first half of launch_lora_xa: only the partial sums.  `t` says where they
+// are and how T [m][rp] comes of them.
+struct XaSums {
+  const float* part;  // [splits][m][rb]; nullptr: no adapter
+  int splits, rb, r, rp;
+  int64_t m;
+  float sigma;
+  uint16_t* T;
+};
+hipError_t launch_lora_xa_sums(const uint16_t* X, int64_t m, int64_t K, const uint16_t* A, int32_t r, int32_t rp,
+                               float sigma, float* part, uint16_t* T, XaSums* t, hipStream_t s);
 // out = sum over rows t < m of Pt[j][t] * Q[t][c] (Pt [rp][mp], zero past m;
 // Q [m][C], C % 8 == 0), fp32 [r][C], or [C][r] with transpose.  `part`
 // holds lora_outer_part_bytes(m, C, r) bytes.
@@ -176,8 +187,9 @@ hipError_t launch_fill_zero_f32(float* p, int64_t count, hipStream_t s);
 // Rows to 8-bit codes and one fp32 scale each: W [n][k] fp32, or X [m][ldx]
 // bf16 of which k columns are used (k % 8 == 0, 16-byte aligned rows).
 hipError_t launch_i8_quant_f32(const float* W, int64_t n, int64_t k, int8_t* Q, float* scales, hipStream_t s);
+// With `t`, also the tokens' adapter product from its partial sums.
 hipError_t launch_i8_quant_bf16(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Q, float* scales,
-                                hipStream_t s);
+                                const XaSums& t, hipStream_t s);
 hipError_t launch_i8_dequant(const WView& w, uint16_t* out, hipStream_t s);
 // Weights that multiply the same tokens in one launch.
 struct I8Set {
@@ -188,7 +200,7 @@ struct I8Set {
   int64_t ldy[kGemvMaxGroup];
   int n[kGemvMaxGroup];
   int tile_end[kGemvMaxGroup];  // weight i owns the row tiles [tile_end[i-1], tile_end[i])
-  int64_t n_end[kGemvMaxGroup];  // channels of weights 0 .. i
+  int64_t n_end[kGemvMaxGroup];  // channels of weights 0 .. i, each rounded up to 4
   int count;
 };
 I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count);
