@@ -39,30 +39,16 @@ struct DxSet {
   int count;
 };
 
-// Columns kb .. kb + 4 N - 1 of token mr from their sums, + G . A of the adapters.
+// dX at o from 4 N sums.
 template <int N>
-__device__ __forceinline__ void store_dx(float (&v)[4 * N], int mr, int kb, int k, uint16_t* __restrict__ dX, const LoraDx& lora) {
-  if (lora.g != nullptr) {
-    for (int j = 0; j < lora.r; ++j) {
-      const float g = __uint_as_float((uint32_t)lora.g[(int64_t)mr * lora.rp + j] << 16);
-      const uint2* ar = reinterpret_cast<const uint2*>(lora.a + (int64_t)j * k + kb);
+__device__ __forceinline__ void store_dx(const float (&v)[4 * N], uint16_t* __restrict__ o) {
 #pragma unroll
-      for (int h = 0; h < N; ++h) {
-        const uint2 a = ar[h];
-        v[4 * h] = fmaf(g, bf16_lo(a.x), v[4 * h]);
-        v[4 * h + 1] = fmaf(g, bf16_hi(a.x), v[4 * h + 1]);
-        v[4 * h + 2] = fmaf(g, bf16_lo(a.y), v[4 * h + 2]);
-        v[4 * h + 3] = fmaf(g, bf16_hi(a.y), v[4 * h + 3]);
-      }
-    }
-  }
-  uint2* o = reinterpret_cast<uint2*>(dX + (int64_t)mr * k + kb);
-#pragma unroll
-  for (int h = 0; h < N; ++h) o[h] = make_uint2(cvt_pk_bf16(v[4 * h], v[4 * h + 1]), cvt_pk_bf16(v[4 * h + 2], v[4 * h + 3]));
+  for (int h = 0; h < N; ++h)
+    reinterpret_cast<uint2*>(o)[h] = make_uint2(cvt_pk_bf16(v[4 * h], v[4 * h + 1]), cvt_pk_bf16(v[4 * h + 2], v[4 * h + 3]));
 }
 
 // Slices [per * blockIdx.y, + per) of the reduction.  `part`: [gridDim.y][m][k]
-// sums instead of dX (then no adapter term).
+// sums instead of dX.
 template <int TM, int U>
 __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int per, uint16_t* __restrict__ dX,
                                                    float* __restrict__ part, LoraDx lora) {
@@ -154,6 +140,35 @@ __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (u < cnt) load(u, first + kWaves * u);
+  // The adapter's G . A, 32 of the rank by each of the first waves (of the first
+  // range), in the columns' order of the weight.  (Added to each output where it
+  // is stored, with scalar sums: m = 300, n = k = 4096, rank 64, all of lbq_lora_bwd 103 us against 67.)
+  if (lora.g != nullptr && blockIdx.y == 0 && 32 * wave < lora.rp) {
+    const int j0 = 32 * wave + 8 * lg;
+    uint2 c[8];  // four columns of row j0 + q
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      c[q] = make_uint2(0u, 0u);
+      if (j0 + q < lora.r) c[q] = *reinterpret_cast<const uint2*>(lora.a + (int64_t)(j0 + q) * k + k0 + 4 * li);
+    }
+    u32x4_t d[TM];
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+      const int64_t mr = min(m0 + 16 * b + li, m - 1);
+      d[b] = *reinterpret_cast<const u32x4_t*>(lora.g + mr * lora.rp + j0);
+    }
+#pragma unroll
+    for (int a = 0; a < TK; ++a) {
+      u32x4_t w;
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        const uint32_t lo = (a < 2 ? c[q].x : c[q].y) >> (16 * (a & 1)), hi = (a < 2 ? c[q + 1].x : c[q + 1].y) >> (16 * (a & 1));
+        w[q >> 1] = (lo & 0xFFFFu) | hi << 16;
+      }
+#pragma unroll
+      for (int b = 0; b < TM; ++b) acc[a][b] = mfma16x16x32(w, d[b], acc[a][b]);
+    }
+  }
   run_ring<U, 2 + L>(cnt, [&](int u, int j) { load(u, first + kWaves * j); }, [&](int u, int) { mma(u); });
 
   f32x4_t* const sums = reinterpret_cast<f32x4_t*>(&ring[wave][0][0]);
@@ -181,12 +196,12 @@ __global__ __launch_bounds__(kThreads) void k_i8_dx(DxSet set, int m, int k, int
     for (int i = 0; i < 4; ++i) o[i] = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
     return;
   }
-  store_dx<4>(v, mr, kb, k, dX, lora);
+  store_dx<4>(v, dX + (int64_t)mr * k + kb);
 }
 
 // dX from the sums of ks ranges: one thread for four columns of a token.
 __global__ __launch_bounds__(256) void k_i8_dx_reduce(const float* __restrict__ part, int ks, int m, int k,
-                                                     uint16_t* __restrict__ dX, LoraDx lora) {
+                                                     uint16_t* __restrict__ dX) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = k / 4;
   if (i >= (int64_t)m * per) return;
@@ -195,8 +210,8 @@ __global__ __launch_bounds__(256) void k_i8_dx_reduce(const float* __restrict__ 
   f32x4_t r = p[0];
 #pragma unroll 3
   for (int j = 1; j < ks; ++j) r += p[j * stride];
-  float v[4] = {r[0], r[1], r[2], r[3]};
-  store_dx<1>(v, (int)(i / per), 4 * (int)(i % per), k, dX, lora);
+  const float v[4] = {r[0], r[1], r[2], r[3]};
+  store_dx<1>(v, dX + 4 * i);
 }
 
 template <int TM, int U>
@@ -287,7 +302,7 @@ hipError_t launch_i8_dx(const WView* ws, const uint16_t* const* dys, int count, 
   else launch<4, 3>(set, m, k, c.ks, c.per, dX, part, lora, s);
   if (part != nullptr)
     hipLaunchKernelGGL(k_i8_dx_reduce, dim3((unsigned)((m * (k / 4) + 255) / 256)), dim3(256), 0, s, part, c.ks, (int)m,
-                       (int)k, dX, lora);
+                       (int)k, dX);
   return hipGetLastError();
 }
 

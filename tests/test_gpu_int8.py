@@ -522,6 +522,26 @@ def test_lora_backward(L):
     assert (np.abs(host(dB) - dY.T @ T) <= tolB).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 64, 64), (3, 2048, 128), (17, 64, 4096), (40, 1024, 1024), (70, 192, 192), (700, 320, 320)])
+@pytest.mark.parametrize("r", [1, 13, 32, 64])
+def test_lora_backward_input_gradient(L, m, n, k, r):
+    """The input gradient with its adapter term, where the reduction is split over
+    waves, workgroups and ranges, and ranks that end inside a step of 32."""
+    sigma = 0.5
+    qw, (q, s) = weight(L, 195, n, k)
+    a, b = lora_parts(r, n, k, r)
+    x, dy = tokens(1, m, k), SI.bf16_normal(2, (m, n), 0.1)
+    dX, _, _ = L.lbq_lora_bwd(to_dev_bf16(x), to_dev_bf16(dy), qw, to_dev_bf16(a), to_dev_bf16(b), sigma)
+    W = O.bf16_to_f64(I8.dequant_bf16(q, s))
+    dY, A, B = (O.bf16_to_f64(v) for v in (dy, a, b))
+    G = sigma * dY @ B
+    g_err = (HALF + (n + 4) * E32) * np.abs(G) + (n + 4) * E32 * sigma * np.abs(dY) @ np.abs(B)
+    ref = dY @ W + G @ A
+    inner = g_err @ np.abs(A) + 2 * (n + r + 4) * E32 * (np.abs(dY) @ np.abs(W) + np.abs(G) @ np.abs(A))
+    tol = inner + HALF * (np.abs(ref) + inner) + 1e-38
+    assert (np.abs(O.bf16_to_f64(bf16_bits_host(dX)) - ref) <= tol).all()
+
+
 def test_training_step(L):
     """An adapted 8-bit layer trained for a few steps as a program does it:
     forward, backward, clipping, optimizer.  Each step's norm is that of its
