@@ -277,7 +277,7 @@ hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys,
                   const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, const lbq::XaSums& t, void* ws, hipStream_t s) {
   const int64_t k = w[0].k;
   const lbq::I8Set set = lbq::i8_set(w, ys, ldys, rows, count);
-  if (lbq::i8_decode_fits(m, k)) return lbq::launch_i8_decode(set, X, m, k, lora, s);
+  if (lbq::i8_decode_fits(m, k)) return lbq::launch_i8_decode(set, X, m, k, lora, t, s);
   uint8_t* p = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(p);
   float* xs = reinterpret_cast<float*>(p + align16((size_t)m * (size_t)k));
@@ -840,7 +840,7 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
   void* part = static_cast<uint8_t*>(workspace) + lora_t_bytes(m, r);
   const lbq::LoraEpi lora{T, B, r, rp};
   const lbq::WView w = view_of(desc, q);
-  if (desc->format == LBQ_INT8 && !lbq::i8_decode_fits(m, desc->k)) {
+  if (desc->format == LBQ_INT8) {
     lbq::XaSums t;
     hipError_t e = lbq::launch_lora_xa_sums(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, &t, s);
     if (e == hipSuccess)

@@ -217,7 +217,8 @@ hipError_t launch_i8_skinny(const I8Set& set, int t, const int8_t* Xq, const flo
 // From bf16 tokens X [m][k] in one launch: m <= 4 and m * k <= kI8DecodeCodes.
 constexpr int kI8DecodeCodes = 16384;
 inline bool i8_decode_fits(int64_t m, int64_t k) { return m <= 4 && m * k <= kI8DecodeCodes; }
-hipError_t launch_i8_decode(const I8Set& set, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora, hipStream_t s);
+hipError_t launch_i8_decode(const I8Set& set, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora, const XaSums& t,
+                            hipStream_t s);
 
 // Input gradient of 1 <= count <= kGemvMaxGroup 8-bit weights of one k, summed
 // (the LoRA term only with count 1).  `part` takes i8_dx_workspace_bytes()
