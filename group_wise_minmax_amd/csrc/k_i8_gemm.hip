@@ -241,7 +241,6 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   uint16_t* Y = set.y[wi];
   const int32_t* rows = set.rows[wi];
   const int64_t ldy = set.ldy[wi];
-  const bool vec = rows == nullptr && (ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(Y) & 15) == 0;
   // A lane's values lie in one token each, four channels of it: stored from here
   // they are 32-byte runs.  Through LDS (16 tokens at a time, in the wave's own
   // part) a token's TN * 16 channels of the wave follow one another, 16 bytes a
@@ -266,10 +265,10 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
     }
     const int mr = m0 + (wm * TM + b) * 16 + lane / C;
     uint16_t* y = Y + (int64_t)mr * ldy;
-    if (vec && nb + 8 <= n) {
+    if (rows == nullptr && nb + 8 <= n) {
 #pragma unroll
       for (int i = 0; i < 16 / R; ++i)
-        if (mr + i * R < m) *reinterpret_cast<u32x4_t*>(y + (int64_t)i * R * ldy + nb) = v[i];
+        if (mr + i * R < m) *reinterpret_cast<u32x4_any_t*>(y + (int64_t)i * R * ldy + nb) = v[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 16 / R; ++i)

@@ -176,6 +176,19 @@ def test_forward_leaves_the_rest_alone(L, m):
     assert (got == -7.0).all()
 
 
+@pytest.mark.parametrize("m", [1, 6, 50, 129, 600])
+@pytest.mark.parametrize("first,ld", [(1, 311), (3, 312), (2, 315)])
+def test_outputs_at_any_address(L, m, first, ld):
+    """Rows that begin at any multiple of two bytes, an odd number of values apart."""
+    n, k = 301, 704
+    qw, (wq, ws) = weight(L, 6, n, k)
+    x = tokens(2, m, k)
+    buf = torch.full((m, ld), -7.0, dtype=torch.bfloat16, device=DEV)
+    L.lbq_linear_fwd(to_dev_bf16(x), qw, out=buf[:, first:first + n])
+    bits_equal(buf[:, first:first + n], I8.product_bf16(*I8.tokens(x), wq, ws))
+    assert (buf[:, :first] == -7.0).all() and (buf[:, first + n:] == -7.0).all()
+
+
 @pytest.mark.parametrize("m", [1, 2, 4, 7, 70, 300])
 def test_longest_rows_of_largest_codes(L, m):
     """k = 2^17 codes of 127: sums just below 2^31, of either sign."""
