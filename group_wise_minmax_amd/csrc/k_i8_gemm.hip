@@ -283,9 +283,12 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
 
 // Tiles of one launch: 256 x 256 outputs each, numbered over all the weights'
 // row tiles; the first `whole` of them by one workgroup each, the others cut
-// into `cut` pieces (2: 128 x 256, 4: 128 x 128).  With ks > 1 (only where
-// nothing is whole) K is split into ks ranges of `per` steps, gridDim.y of them,
-// whose integer sums k_i8_reduce adds.
+// into `cut` pieces (2: 128 x 256, 4: 128 x 128).  With whole = 0 the pieces
+// themselves are numbered, nx x ny of them: workgroups that find their piece
+// past the end would leave the others to a part of the chip, since workgroups
+// go round the shader engines in turn (m = 128, n = 18965, k = 2624: 42.1 us
+// against 25.2).  With ks > 1 (only where nothing is whole) K is split into ks
+// ranges of `per` slices, gridDim.y of them, whose integer sums k_i8_reduce adds.
 struct I8Plan {
   int nx, ny;
   int whole, cut;
@@ -300,15 +303,17 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan p
   const int bid = blockIdx.x;
   const bool whole = bid < plan.whole;
   const int t = whole ? xcd_order(bid, plan.whole) : xcd_order(bid - plan.whole, gridDim.x - plan.whole);
-  const int piece = whole ? 0 : t % plan.cut;
+  const bool pieces = plan.whole == 0;
+  const int piece = whole || pieces ? 0 : t % plan.cut;
   int tx, ty;
-  tile_at(whole ? t : plan.whole + t / plan.cut, plan.nx, plan.ny, tx, ty);
+  tile_at(whole || pieces ? t : plan.whole + t / plan.cut, plan.nx, plan.ny, tx, ty);
   int wi = 0;
 #pragma unroll
   for (int i = 1; i < kGemvMaxGroup; ++i)
     if (i < set.count && tx >= set.tile_end[i - 1]) wi = i;
   if (wi > 0) tx -= set.tile_end[wi - 1];
-  const int n0 = tx * 256 + 128 * (piece & 1), m0 = ty * 256 + 128 * (piece >> 1);
+  const int n0 = tx * (pieces ? 128 : 256) + 128 * (piece & 1);
+  const int m0 = ty * (pieces && plan.cut == 4 ? 128 : 256) + 128 * (piece >> 1);
   if (n0 >= set.n[wi] || m0 >= m) return;
   const int s0 = blockIdx.y * plan.per, steps = min(k / I8K - s0, plan.per);
   if (part != nullptr) part += (int64_t)m * ((int64_t)blockIdx.y * set.n_end[set.count - 1] + (wi == 0 ? 0 : set.n_end[wi - 1]));
@@ -346,52 +351,69 @@ struct I8Choice {
 };
 
 // The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 170 products (m 1 to 3000, n 256 to 20000, k 256 to 28672, weights
-// not in cache): on these the choice is 7% off the best one on average.
-//  * k_i8_skinny: a workgroup takes 0.0125 us for a KiB of operands, and with r
-//    workgroups a CU these share its L1: 0.019 us a KiB and workgroup.  (Its tokens
-//    are the grid's second dimension, which has 65535 workgroups.)
-//  * k_i8_gemm: a round of 256 x 256 tiles (one a CU) takes 0.8 us for 64 of k; a
-//    last round that would leave half of the chip idle is cut into 128 x 256
-//    pieces (0.26 us), one that would leave three quarters idle into 128 x 128
-//    pieces (0.204 us).  Where nothing is whole and the pieces leave CUs idle, K
-//    may be split: the integer sums cost a second launch and 0.86 us for a MB.
+// them on 500 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
+// cache): on these the choice is 1.5% off the best one on average.
+//  * k_i8_skinny: rounds of one workgroup a CU (T = 1: two, by their LDS), each
+//    at a rate for a 128-byte line of a wave that grows with the CUs at work.  (Its
+//    tokens are the grid's second dimension, which has 65535 workgroups.)
+//  * k_i8_gemm: the same with a rate for 64 of k: in 256 x 256 tiles whose last
+//    round is cut where it would leave half of the chip idle (128 x 256 pieces) or
+//    three quarters (128 x 128), or all in tiles or pieces of one size; 128 x 128
+//    pieces may split K, which costs a second launch and the traffic of the sums.
 constexpr int64_t kMostGridY = 65535;
 
 I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
+  // us of `groups` workgroups, `room` of them at a time: each costs `steps` steps
+  // of `step` and `share` where all of the room is taken
+  const auto rounds = [](double groups, int room, double start, double step, double share, double steps) {
+    const double r = groups / room, full = std::floor(r);
+    double us = full * (start + steps * (step + share));
+    if (r > full) us += start + steps * (step + share * (r - full));
+    return us;
+  };
   I8Choice best{1, {}};
   double least = 1e30;
-  for (int t = 1; t <= 4; t *= 2) {
+  static constexpr double kBase[3] = {2.16, 1.76, 1.30}, kStart[3] = {0.44, 0.78, 1.81}, kLine[3] = {0.320, 0.795, 1.663},
+                          kShare[3] = {0.743, 0.516, 1.108}, kRead[3] = {0.1125e-6, 0.100e-6, 0.107e-6};
+  int64_t n = 0, tiles = 0;
+  for (int i = 0; i < count; ++i) n += ns[i], tiles += ceil_div(ns[i], 256) * ceil_div(m, 256);
+  for (int i = 0; i < 3; ++i) {
+    const int t = 1 << i;
     int64_t groups = 0;
     if (ceil_div(m, 16 * t) > kMostGridY) continue;
-    for (int i = 0; i < count; ++i) groups += ceil_div(ns[i], 16 * t);
+    for (int j = 0; j < count; ++j) groups += ceil_div(ns[j], 16 * t);
     groups *= ceil_div(m, 16 * t);
-    const double r = (double)groups / 256, kib = 2.0 * t * 16 * k / 1024;
-    const double us = 2.5 + kib * (0.0125 + 0.019 * r) + (t == 1 ? 0.45 : t == 2 ? 1.5 : 3.4) * r;
+    const double us = kBase[i] + rounds((double)groups, t == 1 ? 512 : 256, kStart[i], kLine[i], kShare[i], (double)ceil_div(k, 1024)) +
+                      kRead[i] * (double)n * k;
     if (us < least) least = us, best.skinny = t;
   }
-  I8Plan p{};
-  int64_t n = 0, pieces = 0;
-  for (int i = 0; i < count; ++i) {
-    p.nx += (int)ceil_div(ns[i], 256);
-    pieces += ceil_div(ns[i], 128) * ceil_div(m, 128);
-    n += ns[i];
-  }
-  p.ny = (int)ceil_div(m, 256);
-  const int64_t tiles = (int64_t)p.nx * p.ny, rest = tiles % 256;
   const int slices = (int)(k / I8K);
-  p.whole = (int)(rest <= 128 ? tiles - rest : tiles);
-  p.cut = rest <= 64 ? 4 : 2;
-  if (p.whole > 0) pieces = rest * p.cut;
+  const auto plan = [&](int64_t whole, int cut) {
+    I8Plan p{};
+    const int tn = whole > 0 ? 256 : 128;
+    for (int i = 0; i < count; ++i) p.nx += (int)ceil_div(ns[i], tn);
+    p.ny = (int)ceil_div(m, whole > 0 || cut == 2 ? 256 : 128);
+    p.whole = (int)whole, p.cut = cut, p.ks = 1, p.per = slices;
+    return p;
+  };
+  const auto consider = [&](I8Plan p) {
+    const int64_t pieces = p.whole > 0 ? (tiles - p.whole) * p.cut : (int64_t)p.nx * p.ny;
+    double us = 3.3 + (double)(n + m) * k * 0.072e-6 + rounds(p.whole, 256, 7.95, 0.340, 0.423, slices);
+    us += p.cut == 2 ? rounds((double)pieces, 256, 3.66, 0.282, 0.173, slices)
+                     : rounds((double)pieces * p.ks, 256, 2.23, 0.172, 0.0985, p.per);
+    if (p.ks > 1) us += 3.2 + 0.45e-6 * 4 * p.ks * m * n;
+    if (us < least) least = us, best.skinny = 0, best.plan = p;
+  };
+  const int64_t rest = tiles % 256;
+  if (tiles > 256 && rest > 0 && rest <= 128) consider(plan(tiles - rest, rest <= 64 ? 4 : 2));
+  consider(plan(tiles, 2));
+  consider(plan(0, 2));
   for (int ks = 1; ks <= 8; ++ks) {
-    if (ks > 1 && (p.whole > 0 || p.cut != 4 || slices < 8 * ks)) break;
+    if (ks > 1 && (tiles > 64 || slices < 4 * ks)) break;
+    I8Plan p = plan(0, 4);
     p.per = (int)ceil_div(slices, ks);
     p.ks = (int)ceil_div(slices, p.per);
-    double us = 3.3 + (double)(n + m) * k * 0.22e-6;
-    us += std::ceil(p.whole / 256.0) * (15.5 + 0.8 * slices);
-    if (p.whole < tiles) us += p.cut == 2 ? 11.4 + 0.26 * slices : std::ceil(pieces * p.ks / 256.0) * (2.3 + 0.204 * p.per);
-    if (p.ks > 1) us += 2.8 + 0.86e-6 * 4 * p.ks * m * n;
-    if (us < least) least = us, best.skinny = 0, best.plan = p;
+    consider(p);
   }
   return best;
 }
@@ -430,15 +452,15 @@ hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs
   int end = 0, most = 0;
   for (int i = 0; i < set.count; ++i) {
     ns[i] = set.n[i];
-    end += (int)ceil_div(set.n[i], 256);
-    set.tile_end[i] = end;
     most = std::max(most, set.n[i]);
   }
   const I8Choice c = choose(ns, set.count, k, m);
   if (c.skinny != 0) return launch_i8_skinny(set, c.skinny, Xq, xs, m, k, lora, s);
   const I8Plan& plan = c.plan;
+  for (int i = 0; i < set.count; ++i) set.tile_end[i] = end += (int)ceil_div(set.n[i], plan.whole > 0 ? 256 : 128);
   int* part = plan.ks > 1 ? static_cast<int*>(work) : nullptr;
-  const dim3 grid((unsigned)(plan.whole + (plan.nx * plan.ny - plan.whole) * plan.cut), (unsigned)plan.ks);
+  const int tiles = plan.nx * plan.ny;
+  const dim3 grid((unsigned)(plan.whole > 0 ? plan.whole + (tiles - plan.whole) * plan.cut : tiles), (unsigned)plan.ks);
   if (lora.t != nullptr && plan.ks == 1)
     hipLaunchKernelGGL(k_i8_gemm<true>, grid, dim3(kGemmThreads), 0, s, set, plan, Xq, xs, (int)m, (int)k, lora, part);
   else
