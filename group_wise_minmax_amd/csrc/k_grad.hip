@@ -3,17 +3,22 @@
 //   norm = (sum over all tensors of x^2)^(1/2), or max |x|;
 //   c = min(1, max_norm / (norm + 1e-6));  out = g * c.
 //
-// Two launches for each group of tensors (their table travels in the kernel's
-// arguments, so nothing is copied to the device and a captured launch keeps
-// it): the first sums, the second scales.  Bound by memory: the gradients are
-// read twice and written once; a set within the 256 MB Infinity Cache is read
-// the second time from there.
+// Two launches for each table of up to 120 tensors (the table travels in the
+// kernel's arguments, so nothing is copied to the device and a captured launch
+// keeps it): one sums, one scales; with several tables one more launch adds up
+// all the partial sums.  Bound by memory: the gradients are read twice and
+// written once.  448 adapter gradients of rank 64 (671 MB): 400 us, the sums at
+// 5.1 TB/s and the scaling at 4.7 (read and written; a copy runs at 5.05).  The
+// scaling walks back from what the sums read last, which is still in the 256 MB
+// Infinity Cache (that table 43 us, the others 71).  Few small tensors are bound
+// by the two launches (4 of rank 16, 0.9 MB: 12.4 us a call, most of it on the
+// host).
 //
 // The squares are summed in fp64 (a square of any finite fp32 value is
 // finite there, and 10^9 of them lose nothing that fp32 could show).  Each
 // workgroup owns a fixed run of 16-KiB pieces of the tensors laid end to end,
-// and every workgroup of the second launch adds the partial sums in the same
-// fixed order: the result does not change from run to run.
+// and whoever adds the partial sums does it in one fixed order: the result does
+// not change from run to run.
 #include "lbq_device.h"
 
 namespace lbq {

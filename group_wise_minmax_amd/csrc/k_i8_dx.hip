@@ -8,7 +8,10 @@
 // 64-byte runs for the L1), and the waves' fp32 sums are added at the end in a
 // fixed order.  Given a workspace, the rows are also split over workgroups,
 // whose sums k_i8_dx_reduce adds: a CU keeps some 0.25 cache lines a ns coming,
-// so a weight needs all of them (m = 40, n = k = 4096: 64 workgroups).
+// so a weight needs all of them (m = 40, n = k = 4096: 64 workgroups 24.7 us, split
+// into four ranges 13.9; by k_bwd_dx's 128 x 128 tiles 108).  Bound by latency:
+// 17 MB at 5 TB/s are 3.4 us, and a launch, a wave's few loads and the second
+// launch follow one another.
 //
 // The reduction runs along W's rows, so an MFMA (v_mfma_f32_16x16x32_bf16) wants
 // 8 rows of one column from a lane, while memory has a row's columns side by

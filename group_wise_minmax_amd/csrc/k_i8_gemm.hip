@@ -4,9 +4,25 @@
 // on v_mfma_i32_16x16x64_i8.  acc is exact in 32-bit integers (k <= 2^17:
 // 127 * 127 * 2^17 < 2^31), so the result does not depend on the order of the
 // sum, on the tile or on how K is split: every kernel here gives the same bits.
+//
+// A workgroup (one a CU, eight waves) computes 256 x 256 outputs, or a piece of
+// that where the tiles leave CUs idle; K goes through four LDS stages of 64 codes,
+// loaded straight to LDS three steps ahead.  What bounds it:
+//  * large products the card's power: the MFMAs alone run at 4.9 POP/s on zeros
+//    and at 4.0 on random codes (32 x 32 x 32 shapes: 3.45, they take more power);
+//    m = 4096, n = 14336, k = 4096 200 us (2.4 POP/s; the library's product 217 to
+//    235), m = n = k = 8192 415 us, and 320 us with all codes 0.  Each wave takes
+//    128 x 64, so that its LDS reads (12 KiB for 32 MFMAs) fit under them; four
+//    waves of 128 x 128 needed more registers than there are without moving
+//    accumulators (337 us).
+//  * pieces the operands: 80 to 92 bytes a ns come to a CU from L2 (m = 333, n = k
+//    = 8192 40.6 us).  Fewer LDS reads (64 x 64 a wave, two groups of waves that
+//    take a slice each) and operands read a whole step ahead gained nothing: 41.3
+//    and 45.5 us.
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"
+
 #include <algorithm>
 #include <cmath>
 
@@ -14,8 +30,9 @@ namespace lbq {
 
 namespace {
 
-// 64 codes of K of a tile in LDS: BN rows of W and BM rows of X, 64 bytes each.
-// chunks in the order of i8_key.
+// 64 codes of K of a tile in LDS: BN rows of W and BM rows of X, 64 bytes each, in
+// the order of i8_key (no bank conflicts; rows in plain order have 2.2e7 conflict
+// cycles in m = 4096, n = 14336, k = 4096).
 template <int BN, int BM>
 struct I8Stage {
   int8_t w[BN * 64];
@@ -51,7 +68,8 @@ constexpr int kGemmOut = 1 << 15;  // and for the outputs on their way to memory
 constexpr int kStages = 4;
 // A K step of a tile, one stage in LDS, is KS slices of 64 codes: the barrier
 // of a step costs some 300 cycles, so a step holds at least 512 cycles of a
-// SIMD's MFMAs (128 x 128 tiles: 2 slices, k = 4096 22 -> 1x us).
+// SIMD's MFMAs (128 x 128 pieces: 2 slices; m = 130, n = k = 4096 22.6 -> 20.2 us,
+// m = 333, n = k = 8192 50.7 -> 42.0).
 template <int BN, int BM>
 constexpr int i8_slices() {
   return kStages * 2 * (int)sizeof(I8Stage<BN, BM>) <= kGemmLds ? 2 : 1;

@@ -12,7 +12,8 @@
 //
 // Bound by memory: a row of up to 32768 values is read once and kept in registers
 // between the search for its largest magnitude and the codes; a longer row is
-// read again, from L2.
+// read again, from L2.  m = k = 4096: 10.2 us (4.9 TB/s); a few rows are bound by
+// their latency (3 rows of 28672: 5.5 us).
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"
@@ -56,7 +57,9 @@ struct Chunk8<uint16_t> {
 // One workgroup of NT threads a row.  NC: chunks of 8 values a thread keeps
 // (k <= 8 * NT * NC).  The row's adapter product comes along (NT >= rp): its
 // partial sums are loaded behind the row, which saves their own launch (m =
-// 2048, n = k = 4096, rank 16 63.8 -> 60.9 us; m = 64, rank 64 29.9 -> 23.9).  row0: the first row's place in t.
+// 2048, n = k = 4096, rank 16 63.8 -> 60.9 us; m = 64, rank 64 29.9 -> 23.9; the
+// whole product X A^T in this kernel, from the same registers, was slower: 65.8).
+// row0: the first row's place in t.
 template <typename T, int NT, int NC, bool KEEP>
 __global__ __launch_bounds__(NT) void k_i8_quant_rows(const T* __restrict__ X, int64_t ldx, int64_t k,
                                                      int8_t* __restrict__ Q, float* __restrict__ scales, XaSums t,

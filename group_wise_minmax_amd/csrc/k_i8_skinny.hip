@@ -11,11 +11,14 @@
 // m = 512, n = k = 4096 37.5 -> 29.3 us through LDS; with lines of 64 bytes the
 // two halves of a line are fetched by two waves: m = 3, n = 8192, k = 28672
 // 54.8 -> 49.1 us with whole lines.)  The waves' integer sums are added at the
-// end: exact, so no split changes a bit, and no second launch is needed.
+// end: exact, so no split changes a bit, and no second launch is needed.  Bound
+// by memory where the weight is large (m = 3, n = 8192, k = 28672: 235 MB in 47 us,
+// 5.0 TB/s; m = 24, n = 14336, k = 4096: 60 MB in 14), by latency where it is
+// small.
 //
 // k_i8_decode is the same for up to 4 tokens that are short enough to be
 // quantized by every workgroup for itself while its first weights are on
-// their way: one launch from bf16 tokens to outputs.
+// their way: one launch from bf16 tokens to outputs (m = 1, n = k = 4096: 6.6 us).
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"

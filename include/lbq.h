@@ -104,8 +104,9 @@ typedef struct {
  *                              code 2i in bits 7..4 and code 2i+1 in bits 3..0
  *                              [BNB]; 2-bit: code 4i in bits 7..6, then 5..4,
  *                              3..2, 1..0; INT8: i8[n][k], the codes
- *                              themselves.  Only the bytes matter: the caller
- *                              may hold them in any dtype of the same size.
+ *                              themselves, in [-127, 127].  Only the bytes
+ *                              matter: the caller may hold them in any dtype of
+ *                              the same size.
  *   scales        MINMAX       f32[n][k/group]; compact: fp16 bit patterns
  *                              u16[n][k/group] (2-byte aligned)
  *                 INT8         f32[n]
