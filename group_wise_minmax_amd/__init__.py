@@ -169,15 +169,9 @@ class QuantizedWeight:
     def qtensor(self) -> QTensor:
         if self.desc.format == LBQ_INT8:
             self._check_int8()
-        q = QTensor()
-        q.packed = _ptr(self.packed)
-        q.scales = _ptr(self.scales)
-        q.zeros = _ptr(self.zeros)
-        q.absmax = _ptr(self.absmax)
-        q.absmax_q = _ptr(self.absmax_q)
-        q.absmax_scale = _ptr(self.absmax_scale)
-        q.out_rows = _ptr(self.out_rows)
-        return q
+            return QTensor(packed=self.packed.data_ptr(), scales=self.scales.data_ptr(), out_rows=_ptr(self.out_rows))
+        return QTensor(_ptr(self.packed), _ptr(self.scales), _ptr(self.zeros), _ptr(self.absmax), _ptr(self.absmax_q),
+                       _ptr(self.absmax_scale), _ptr(self.out_rows))
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -294,8 +288,9 @@ def lbq_linear_fwd(X: torch.Tensor, qw: QuantizedWeight, out: Optional[torch.Ten
     if out is None:
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
-        out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
-    _need_out(out, m, qw)
+        out = X.new_empty((m, qw.n))
+    else:
+        _need_out(out, m, qw)
     nbytes = lbq_linear_workspace_bytes(qw, m)
     if workspace is None:
         workspace = _ws(nbytes, X.device)
@@ -318,8 +313,9 @@ def lbq_linear_fwd_noalloc(X: torch.Tensor, qw: QuantizedWeight, out: Optional[t
     if out is None:
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
-        out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
-    _need_out(out, m, qw)
+        out = X.new_empty((m, qw.n))
+    else:
+        _need_out(out, m, qw)
     q = qw.qtensor()
     _same_device(X.device, qw.packed, out)
     with _on(X.device):
@@ -374,17 +370,25 @@ def lbq_linear_bwd_dx(dY: torch.Tensor, qw: QuantizedWeight, out: Optional[torch
                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = dY . deq(W) in bf16 (see ``lbq_linear_bwd_dx`` in lbq.h; an INT8
     weight runs as ``lbq_linear_bwd_dx_grouped_ws``)."""
-    if qw.desc.format == LBQ_INT8:
-        return lbq_linear_bwd_dx_grouped([dY], [qw], out, workspace)
     _need(dY, "dY", torch.bfloat16)
     if dY.dim() != 2 or dY.shape[1] != qw.n:
         raise ValueError(f"dY must be [m, {qw.n}]")
     m = dY.shape[0]
     if out is None:
-        out = torch.empty((m, qw.k), dtype=torch.bfloat16, device=dY.device)
-    _need(out, "out", torch.bfloat16, (m, qw.k))
+        out = dY.new_empty((m, qw.k))
+    else:
+        _need(out, "out", torch.bfloat16, (m, qw.k))
     q = qw.qtensor()
-    _same_device(dY.device, qw.packed, out)
+    _same_device(dY.device, qw.packed, out, workspace)
+    if qw.desc.format == LBQ_INT8:
+        desc, dp = ctypes.byref(qw.desc), ctypes.c_void_p(dY.data_ptr())
+        if workspace is None:
+            workspace = _ws(lib.lbq_linear_bwd_dx_grouped_workspace_bytes(1, desc, m), dY.device)
+        with _on(dY.device):
+            check(lib.lbq_linear_bwd_dx_grouped_ws(1, desc, ctypes.byref(q), ctypes.byref(dp), m, out.data_ptr(), _ptr(workspace),
+                                                   0 if workspace is None else workspace.numel(), _stream(dY.device)),
+                  "lbq_linear_bwd_dx_grouped_ws")
+        return out
     with _on(dY.device):
         check(lib.lbq_linear_bwd_dx(ctypes.byref(qw.desc), ctypes.byref(q), dY.data_ptr(), m,
                                     out.data_ptr(), _stream(dY.device)), "lbq_linear_bwd_dx")
@@ -443,8 +447,9 @@ def lbq_lora_fwd(X: torch.Tensor, qw: QuantizedWeight, A: torch.Tensor, B: torch
     if out is None:
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
-        out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=X.device)
-    _need_out(out, m, qw)
+        out = X.new_empty((m, qw.n))
+    else:
+        _need_out(out, m, qw)
     nbytes = lbq_lora_workspace_bytes(qw, m, r)
     if workspace is None:
         workspace = _ws(nbytes, X.device)
@@ -557,11 +562,13 @@ def lbq_quantize_tokens(X: torch.Tensor, out=None):
     m, k = X.shape
     if k > 1 and X.stride(1) != 1:
         raise ValueError("X must have unit column stride")
-    codes, scales = out if out is not None else (torch.empty((m, k), dtype=torch.int8, device=X.device),
-                                                 torch.empty(m, dtype=torch.float32, device=X.device))
-    _need(codes, "codes", torch.int8, (m, k))
-    _need(scales, "scales", torch.float32, (m,))
-    _same_device(X.device, codes, scales)
+    if out is None:
+        codes, scales = X.new_empty((m, k), dtype=torch.int8), X.new_empty(m, dtype=torch.float32)
+    else:
+        codes, scales = out
+        _need(codes, "codes", torch.int8, (m, k))
+        _need(scales, "scales", torch.float32, (m,))
+        _same_device(X.device, codes, scales)
     ldx = X.stride(0) if m > 1 else k
     with _on(X.device):
         check(lib.lbq_quantize_tokens(X.data_ptr(), m, k, ldx, codes.data_ptr(), scales.data_ptr(), _stream(X.device)),
@@ -583,7 +590,8 @@ def lbq_linear_fwd_tokens(codes: torch.Tensor, scales: torch.Tensor, qw: Quantiz
         if qw.out_rows is not None:
             raise ValueError("out must be given when out_rows is set")
         out = torch.empty((m, qw.n), dtype=torch.bfloat16, device=dev)
-    _need_out(out, m, qw)
+    else:
+        _need_out(out, m, qw)
     _same_device(dev, scales, out, qw.packed, workspace)
     if workspace is None:
         workspace = _ws(lib.lbq_linear_fwd_tokens_workspace_bytes(ctypes.byref(qw.desc), m), dev)
