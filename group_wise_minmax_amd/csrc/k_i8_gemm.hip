@@ -380,7 +380,7 @@ struct I8Choice {
 //    pieces may split K, which costs a second launch and the traffic of the sums.
 constexpr int64_t kMostGridY = 65535;
 
-I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
+I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
   // us of `groups` workgroups, `room` of them at a time: each costs `steps` steps
   // of `step` and `share` where all of the room is taken
   const auto rounds = [](double groups, int room, double start, double step, double share, double steps) {
@@ -427,7 +427,7 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
   consider(plan(tiles, 2));
   consider(plan(0, 2));
   for (int ks = 1; ks <= 8; ++ks) {
-    if (ks > 1 && (tiles > 64 || slices < 4 * ks)) break;
+    if (ks > 1 && (!split || tiles > 64 || slices < 4 * ks)) break;
     I8Plan p = plan(0, 4);
     p.per = (int)ceil_div(slices, ks);
     p.ks = (int)ceil_div(slices, p.per);
@@ -438,12 +438,15 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m) {
 
 }  // namespace
 
-size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
-  const I8Choice c = choose(ns, count, k, m);
+static size_t part_bytes(const I8Choice& c, const int64_t* ns, int count, int64_t m) {
   if (c.skinny != 0 || c.plan.ks == 1) return 0;
   int64_t n = 0;
   for (int i = 0; i < count; ++i) n += padded((int)ns[i]);
   return (size_t)c.plan.ks * (size_t)m * (size_t)n * sizeof(int);
+}
+
+size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
+  return part_bytes(choose(ns, count, k, m, true), ns, count, m);
 }
 
 I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count) {
@@ -464,7 +467,7 @@ I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const in
 }
 
 hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
-                         const LoraEpi& lora, void* work, hipStream_t s) {
+                         const LoraEpi& lora, void* work, size_t work_bytes, hipStream_t s) {
   I8Set set = weights;
   int64_t ns[kGemvMaxGroup];
   int end = 0, most = 0;
@@ -472,7 +475,8 @@ hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs
     ns[i] = set.n[i];
     most = std::max(most, set.n[i]);
   }
-  const I8Choice c = choose(ns, set.count, k, m);
+  I8Choice c = choose(ns, set.count, k, m, true);
+  if (part_bytes(c, ns, set.count, m) > work_bytes) c = choose(ns, set.count, k, m, false);
   if (c.skinny != 0) return launch_i8_skinny(set, c.skinny, Xq, xs, m, k, lora, s);
   const I8Plan& plan = c.plan;
   for (int i = 0; i < set.count; ++i) set.tile_end[i] = end += (int)ceil_div(set.n[i], plan.whole > 0 ? 256 : 128);

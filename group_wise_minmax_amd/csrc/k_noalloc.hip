@@ -57,12 +57,13 @@ extern "C" lbq_status lbq_linear_fwd_noalloc(const lbq_desc* desc, const lbq_qte
                                              int64_t m, uint16_t* Y, int64_t ldy, void* stream) {
   lbq_status st = lbq::check_fwd(desc, q, X, m, Y, ldy);
   if (st != LBQ_OK) return st;
-  if (m == 0) return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, nullptr, 0, stream, "lbq_linear_fwd_noalloc");
+  if (m == 0) return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, nullptr, 0, true, stream, "lbq_linear_fwd_noalloc");
   // The small-batch kernel's partials are required; the GEMM's K-split
   // partials (m > kSkinnyMaxM) are used when they fit the array, and the
-  // GEMM runs unsplit when they do not.
+  // GEMM runs unsplit when they do not.  So does an INT8 weight's product; the
+  // codes of its tokens are required (linear_fwd_body checks them).
   const size_t need = lbq_linear_workspace_bytes(desc, m);
-  if (m <= lbq::kSkinnyMaxM && need > kScratchBytes) {
+  if (m <= lbq::kSkinnyMaxM && desc->format != LBQ_INT8 && need > kScratchBytes) {
     char buf[160];
     snprintf(buf, sizeof buf, "needs %zu bytes of scratch; the allocation-free forward holds %zu", need,
              kScratchBytes);
@@ -70,6 +71,6 @@ extern "C" lbq_status lbq_linear_fwd_noalloc(const lbq_desc* desc, const lbq_qte
   }
   void* p = nullptr;
   if (need > 0 && (st = scratch_of_current_device(&p)) != LBQ_OK) return st;
-  return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, p, need > 0 ? kScratchBytes : 0, stream,
+  return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, p, need > 0 ? kScratchBytes : 0, true, stream,
                               "lbq_linear_fwd_noalloc");
 }

@@ -274,7 +274,8 @@ size_t i8_workspace(const int64_t* ns, int count, int64_t k, int64_t m) {
   return i8_token_bytes(m, k) + lbq::i8_fwd_workspace_bytes(ns, count, k, m);
 }
 hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* rows, int count,
-                  const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, const lbq::XaSums& t, void* ws, hipStream_t s) {
+                  const uint16_t* X, int64_t m, const lbq::LoraEpi& lora, const lbq::XaSums& t, void* ws,
+                  size_t ws_bytes, hipStream_t s) {
   const int64_t k = w[0].k;
   const lbq::I8Set set = lbq::i8_set(w, ys, ldys, rows, count);
   if (lbq::i8_decode_fits(m, k)) return lbq::launch_i8_decode(set, X, m, k, lora, t, s);
@@ -283,14 +284,14 @@ hipError_t i8_fwd(const lbq::WView* w, uint16_t* const* ys, const int64_t* ldys,
   float* xs = reinterpret_cast<float*>(p + align16((size_t)m * (size_t)k));
   const hipError_t e = lbq::launch_i8_quant_bf16(X, m, k, k, xq, xs, t, s);
   if (e != hipSuccess) return e;
-  return lbq::launch_i8_fwd(set, xq, xs, m, k, lora, p + i8_token_bytes(m, k), s);
+  return lbq::launch_i8_fwd(set, xq, xs, m, k, lora, p + i8_token_bytes(m, k), ws_bytes - i8_token_bytes(m, k), s);
 }
 
 hipError_t dispatch_fwd(const lbq_desc* desc, const lbq::WView& w, const uint16_t* X, int64_t m,
                         uint16_t* Y, int64_t ldy, const int32_t* out_rows,
                         const lbq::LoraEpi& lora, void* ws, size_t ws_bytes, hipStream_t s) {
   const lbq::WKind kind = kind_of(desc);
-  if (kind == lbq::WK_I8) return i8_fwd(&w, &Y, &ldy, &out_rows, 1, X, m, lora, lbq::XaSums{}, ws, s);
+  if (kind == lbq::WK_I8) return i8_fwd(&w, &Y, &ldy, &out_rows, 1, X, m, lora, lbq::XaSums{}, ws, ws_bytes, s);
   if (m == 1) return lbq::launch_gemv1(kind, &w, &Y, &out_rows, 1, X, lora, nf4_table(), s);
   if (use_gemvm(desc, m)) return lbq::launch_gemvm(kind, &w, &Y, &ldy, &out_rows, 1, X, m, lora, nf4_table(), s);
   if (m <= lbq::kSkinnyMaxM)
@@ -361,10 +362,12 @@ lbq_status check_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t*
 // The forward of lbq_linear_fwd once the arguments have passed check_fwd:
 // the workspace check and the dispatch.
 lbq_status linear_fwd_body(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X, int64_t m,
-                           uint16_t* Y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream,
+                           uint16_t* Y, int64_t ldy, void* workspace, size_t ws_bytes, bool scratch, void* stream,
                            const char* who) {
   if (m == 0) return ok();
-  const size_t need = fwd_workspace(desc, m, false);
+  size_t need = fwd_workspace(desc, m, false);
+  // without room for its partial sums an 8-bit product runs unsplit: the same bits
+  if (scratch && need > 0 && desc->format == LBQ_INT8) need = i8_token_bytes(m, desc->k);
   // the partials of the m > 64 GEMM are optional
   if ((m <= lbq::kSkinnyMaxM || desc->format == LBQ_INT8) && need > 0) {
     if (workspace == nullptr || ws_bytes < need)
@@ -434,7 +437,7 @@ lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint
                           void* stream) {
   const lbq_status st = check_fwd_common(desc, q, X, m, Y, ldy);
   if (st != LBQ_OK) return st;
-  return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, workspace, ws_bytes, stream, "lbq_linear_fwd");
+  return lbq::linear_fwd_body(desc, q, X, m, Y, ldy, workspace, ws_bytes, false, stream, "lbq_linear_fwd");
 }
 
 lbq_status lbq_quantize_tokens(const uint16_t* X, int64_t m, int64_t k, int64_t ldx, int8_t* Xq, float* xscale,
@@ -474,7 +477,7 @@ lbq_status lbq_linear_fwd_tokens(const lbq_desc* desc, const lbq_qtensor* q, con
   const lbq::LoraEpi none{nullptr, nullptr, 0, 0};
   const lbq::WView w = view_of(desc, q);
   return hip_status(lbq::launch_i8_fwd(lbq::i8_set(&w, &Y, &ldy, &q->out_rows, 1), Xq, xscale, m, desc->k, none, workspace,
-                                       static_cast<hipStream_t>(stream)),
+                                       ws_bytes, static_cast<hipStream_t>(stream)),
                     "lbq_linear_fwd_tokens");
 }
 
@@ -652,7 +655,7 @@ lbq_status lbq_linear_fwd_grouped(int32_t count, const lbq_desc* descs, const lb
       rows[c] = qs[j].out_rows;
       ++c;
     }
-    if (kind == lbq::WK_I8) e = i8_fwd(ws, ys, lds, rows, c, X, m, none, lbq::XaSums{}, workspace, s);
+    if (kind == lbq::WK_I8) e = i8_fwd(ws, ys, lds, rows, c, X, m, none, lbq::XaSums{}, workspace, ws_bytes, s);
     else if (m == 1) e = lbq::launch_gemv1(kind, ws, ys, rows, c, X, none, nf4_table(), s);
     else if (gemvm) e = lbq::launch_gemvm(kind, ws, ys, lds, rows, c, X, m, none, nf4_table(), s);
     else if (m <= lbq::kSkinnyMaxM)
@@ -842,9 +845,11 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
   const lbq::WView w = view_of(desc, q);
   if (desc->format == LBQ_INT8) {
     lbq::XaSums t;
+    const size_t sums = lbq::lora_xa_part_bytes(m, desc->k, r);
     hipError_t e = lbq::launch_lora_xa_sums(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, &t, s);
     if (e == hipSuccess)
-      e = i8_fwd(&w, &Y, &ldy, &q->out_rows, 1, X, m, lora, t, static_cast<uint8_t*>(part) + lbq::lora_xa_part_bytes(m, desc->k, r), s);
+      e = i8_fwd(&w, &Y, &ldy, &q->out_rows, 1, X, m, lora, t, static_cast<uint8_t*>(part) + sums,
+                 ws_bytes - lora_t_bytes(m, r) - sums, s);
     return hip_status(e, "lbq_lora_fwd");
   }
   const hipError_t e = lbq::launch_lora_xa(X, m, desc->k, A, r, rp, sigma, static_cast<float*>(part), T, nullptr, m, s);

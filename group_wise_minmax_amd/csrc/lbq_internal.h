@@ -206,10 +206,10 @@ struct I8Set {
 I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count);
 // The product on quantized tokens Xq [m][k] with scales xs [m], for up to
 // kGemvMaxGroup weights of one k (the LoRA term only with count 1).  `work`
-// holds i8_fwd_workspace_bytes() bytes.
+// holds i8_fwd_workspace_bytes() bytes; with less K is not split (the same bits).
 size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m);
 hipError_t launch_i8_fwd(const I8Set& set, const int8_t* Xq, const float* xs, int64_t m, int64_t k, const LoraEpi& lora,
-                         void* work, hipStream_t s);
+                         void* work, size_t work_bytes, hipStream_t s);
 // The same by workgroups of 16 t channels and 16 t tokens (t = 1, 2, 4) that
 // split K over their waves; set.tile_end is not looked at.
 hipError_t launch_i8_skinny(const I8Set& set, int t, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
@@ -263,10 +263,11 @@ lbq_status set_error(lbq_status s, const char* what);
 // Argument checks of lbq_linear_fwd (everything but the workspace).
 lbq_status check_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X, int64_t m, uint16_t* Y,
                      int64_t ldy);
-// lbq_linear_fwd after check_fwd: workspace check and dispatch (`who` names
-// the entry point in error details).
+// lbq_linear_fwd after check_fwd: workspace check and dispatch (`scratch`: the
+// workspace is what the library has, not what was asked for; `who` names the
+// entry point in error details).
 lbq_status linear_fwd_body(const lbq_desc* desc, const lbq_qtensor* q, const uint16_t* X, int64_t m,
-                           uint16_t* Y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream,
+                           uint16_t* Y, int64_t ldy, void* workspace, size_t ws_bytes, bool scratch, void* stream,
                            const char* who);
 
 }  // namespace lbq

@@ -233,9 +233,10 @@ lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint
 /* For callers that cannot allocate device memory (work captured into a HIP
  * graph, tight serving loops, harnesses that forbid hipMalloc): the forward
  * of lbq_linear_fwd, the same kernels and the same results bit for bit
- * (except as noted below for m > 64), with no workspace argument.  The only scratch memory the forward uses (the fp32
- * K-split partial sums of the small-batch kernel, 2 <= m <= 64, and of a
- * GEMM that splits K, m > 64) lives in an array of LBQ_NOALLOC_SCRATCH_BYTES
+ * (except as noted below for m > 64), with no workspace argument.  The only
+ * scratch memory the forward uses (the fp32 K-split partial sums of the
+ * small-batch kernel, 2 <= m <= 64, and of a GEMM that splits K, m > 64; the
+ * codes of an INT8 weight's tokens and its partial sums) lives in an array of LBQ_NOALLOC_SCRATCH_BYTES
  * in the library's device image, one per device, held until the process
  * ends; the call allocates and frees nothing.  Arguments, layouts and errors
  * as lbq_linear_fwd; LBQ_E_WORKSPACE when a call with m <= 64 would need
@@ -243,7 +244,9 @@ lbq_status lbq_linear_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint
  * m > 64 a GEMM whose partials do not fit the array runs unsplit, as
  * lbq_linear_fwd does without a workspace (then the results agree with
  * lbq_linear_fwd given its workspace within fp32 rounding, not bit for
- * bit).  The array's device address is looked up on the
+ * bit).  An INT8 product also runs unsplit where its partial sums do not fit
+ * (the same bits); LBQ_E_WORKSPACE when the codes of its tokens, m * (k + 4)
+ * bytes, do not.  The array's device address is looked up on the
  * first call on a device that needs it; that call uses the current device
  * (which must be the stream's).  Every call on a device shares that device's
  * array: calls that overlap on one device (two streams or two host threads)

@@ -283,6 +283,18 @@ def test_noalloc_forward_refuses_what_does_not_fit(L):
     assert e.value.name == "LBQ_E_WORKSPACE"
 
 
+@pytest.mark.parametrize("m,n,k", [(64, 11008, 65536), (250, 8192, 8192)])
+def test_noalloc_forward_without_room_for_partial_sums(L, m, n, k):
+    """The library's array holds the codes but not the partial sums: the same bits."""
+    g = torch.Generator(device=DEV).manual_seed(m)
+    q = torch.randint(-127, 128, (n, k), generator=g, device=DEV, dtype=torch.int8)
+    qw = L.QuantizedWeight(L.make_desc("int8", n, k), q.view(torch.uint8), torch.rand((n, 1), generator=g, device=DEV))
+    X = torch.randn((m, k), generator=g, device=DEV).to(torch.bfloat16)
+    assert m * (k + 4) < 2 ** 24 < L.lbq_linear_workspace_bytes(qw, m)
+    y = L.lbq_linear_fwd(X, qw)
+    assert torch.equal(L.lbq_linear_fwd_noalloc(X, qw), y) and y.float().abs().max() > 0
+
+
 def test_streams_at_once(L):
     """Two weights on two streams in turn, each with its own workspace."""
     k = 2048
