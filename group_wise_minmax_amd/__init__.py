@@ -652,9 +652,9 @@ class LbqGradSet:
         self._seen = seen
 
     def _call(self, norm_type: float, max_norm: Optional[float]) -> torch.Tensor:
-        if float(norm_type) not in _NORM_TYPE:
+        kind = _NORM_TYPE.get(norm_type)
+        if kind is None:
             raise ValueError("norm_type must be 2 or inf")
-        kind = _NORM_TYPE[float(norm_type)]
         self._look()
         norm = torch.empty((), dtype=torch.float32, device=self.device)
         workspace = _ws(self._nbytes, self.device)

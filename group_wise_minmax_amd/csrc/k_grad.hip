@@ -11,7 +11,7 @@
 // 5.1 TB/s and the scaling at 4.7 (read and written; a copy runs at 5.05).  The
 // scaling walks back from what the sums read last, which is still in the 256 MB
 // Infinity Cache (that table 43 us, the others 71).  Few small tensors are bound
-// by the two launches (4 of rank 16, 0.9 MB: 12.4 us a call, most of it on the
+// by the two launches (4 of rank 16, 0.9 MB: 11.6 us a call, most of it on the
 // host).
 //
 // The squares are summed in fp64 (a square of any finite fp32 value is
@@ -88,8 +88,8 @@ __device__ __forceinline__ double take(double acc, float x) {
 // The pieces of this workgroup, one call of f(tensor, first element, end)
 // each: [lo, hi) of the tensors laid end to end, from the first to the last, or
 // from the last to the first.
-template <bool BACK, typename F>
-__device__ __forceinline__ void for_pieces(const GradTable& t, F f) {
+template <bool BACK, int N, typename F>
+__device__ __forceinline__ void for_pieces(const GradTable<N>& t, F f) {
   const int64_t total = t.piece_end[t.count - 1];
   const int lo = (int)(total * blockIdx.x / gridDim.x), hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
   if (lo >= hi) return;
@@ -148,8 +148,8 @@ __device__ __forceinline__ double take_piece(double acc, const void* g, int64_t 
   return acc;
 }
 
-template <bool INF>
-__global__ __launch_bounds__(kThreads) void k_grad_norm(GradTable t, double* __restrict__ part) {
+template <bool INF, int N>
+__global__ __launch_bounds__(kThreads) void k_grad_norm(GradTable<N> t, double* __restrict__ part) {
   double acc = 0.0;
   for_pieces<false>(t, [&](int i, int64_t first, int64_t end) {
     const int dt = t.dtype[i];
@@ -235,8 +235,8 @@ __global__ __launch_bounds__(1024) void k_grad_norm_out(const double* __restrict
 
 // Scales the tensors of a table; the norm from `parts` partial values, or from
 // *norm itself (parts == 0) where a launch before this one has summed them.
-template <bool INF>
-__global__ __launch_bounds__(kThreads) void k_grad_scale(GradTable t, const double* __restrict__ part, int parts,
+template <bool INF, int N>
+__global__ __launch_bounds__(kThreads) void k_grad_scale(GradTable<N> t, const double* __restrict__ part, int parts,
                                                         float max_norm, float* __restrict__ norm) {
   float n;
   if (parts > 0) {
@@ -263,7 +263,7 @@ int64_t pieces_of(const lbq_grad& g) {
 }
 
 // The next table of tensors from `at` on (empty ones left out); false when none is left.
-bool next_table(const lbq_grad* g, int count, int& at, GradTable& t) {
+bool next_table(const lbq_grad* g, int count, int& at, GradTable<kGradTable>& t) {
   t.count = 0;
   int64_t end = 0;
   for (; at < count && t.count < kGradTable; ++at) {
@@ -278,15 +278,32 @@ bool next_table(const lbq_grad* g, int count, int& at, GradTable& t) {
   return t.count > 0;
 }
 
+// f(table) with the table cut to kGradFew where they suffice: the arguments of a
+// launch are written to it (4 tensors, norm and scaling 12.3 us a call against
+// 11.6).
+template <typename F>
+void with_table(const GradTable<kGradTable>& t, F f) {
+  if (t.count > kGradFew) return f(t);
+  GradTable<kGradFew> few;
+  for (int i = 0; i < t.count; ++i) {
+    few.grad[i] = t.grad[i], few.out[i] = t.out[i], few.numel[i] = t.numel[i];
+    few.piece_end[i] = t.piece_end[i], few.dtype[i] = t.dtype[i];
+  }
+  few.count = t.count;
+  f(few);
+}
+
 // Workgroups of a table of p pieces: eight a CU where there are that many.
 int groups_of(int64_t p) { return (int)(p < kGradGroups ? p : kGradGroups); }
 
 template <bool INF>
 hipError_t norm_launches(const lbq_grad* g, int count, double* part, hipStream_t s) {
-  GradTable t;
-  for (int at = 0; next_table(g, count, at, t);) {
-    const int groups = groups_of(t.piece_end[t.count - 1]);
-    hipLaunchKernelGGL(k_grad_norm<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part);
+  GradTable<kGradTable> all;
+  for (int at = 0; next_table(g, count, at, all);) {
+    const int groups = groups_of(all.piece_end[all.count - 1]);
+    with_table(all, [&](const auto& t) {
+      hipLaunchKernelGGL(k_grad_norm<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part);
+    });
     part += groups;
   }
   return hipGetLastError();
@@ -306,12 +323,14 @@ hipError_t scale_launches(const lbq_grad* g, int count, const double* part, int 
   int full = 0;
   for (int i = 0; i < count; ++i) full += g[i].numel > 0;
   for (int first = full > 0 ? (full - 1) / kGradTable * kGradTable : -1; first >= 0; first -= kGradTable) {
-    GradTable t;
+    GradTable<kGradTable> all;
     int at = 0;
     for (int skip = first; skip > 0 || g[at].numel == 0; ++at) skip -= g[at].numel > 0;
-    next_table(g, count, at, t);
-    const int groups = groups_of(t.piece_end[t.count - 1]);
-    hipLaunchKernelGGL(k_grad_scale<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part, parts, max_norm, norm);
+    next_table(g, count, at, all);
+    const int groups = groups_of(all.piece_end[all.count - 1]);
+    with_table(all, [&](const auto& t) {
+      hipLaunchKernelGGL(k_grad_scale<INF>, dim3((unsigned)groups), dim3(kThreads), 0, s, t, part, parts, max_norm, norm);
+    });
   }
   return hipGetLastError();
 }

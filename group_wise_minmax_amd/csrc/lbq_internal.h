@@ -232,14 +232,16 @@ hipError_t launch_bwd_dx_i8_tiles(const WView* ws, const uint16_t* const* dys, i
                                   uint16_t* dX, const LoraDx& lora, hipStream_t s);
 
 // ---- gradient norm (k_grad.hip) -------------------------------------------------
-// Tensors of one launch, in the kernel's arguments (they may take 4 KiB).
-constexpr int kGradTable = 120;
+// Tensors of one launch, in the kernel's arguments (they may take 4 KiB): up to N,
+// kGradTable or, for few, kGradFew.
+constexpr int kGradTable = 120, kGradFew = 16;
+template <int N>
 struct GradTable {
-  const void* grad[kGradTable];
-  void* out[kGradTable];
-  int64_t numel[kGradTable];
-  int piece_end[kGradTable];
-  uint8_t dtype[kGradTable];
+  const void* grad[N];
+  void* out[N];
+  int64_t numel[N];
+  int piece_end[N];
+  uint8_t dtype[N];
   int count;
 };
 constexpr int kGradGroups = 2048;  // most workgroups of a launch, each with a partial value
