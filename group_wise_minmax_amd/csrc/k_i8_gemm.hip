@@ -369,8 +369,8 @@ struct I8Choice {
 };
 
 // The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 500 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
-// cache): on these the choice is 1.5% off the best one on average.
+// them on 700 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
+// cache): on these the choice is 1.8% off the best one on average.
 //  * k_i8_skinny: rounds of one workgroup a CU (T = 1: two, by their LDS), each
 //    at a rate for a 128-byte line of a wave that grows with the CUs at work.  (Its
 //    tokens are the grid's second dimension, which has 65535 workgroups.)
@@ -391,8 +391,8 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
   };
   I8Choice best{1, {}};
   double least = 1e30;
-  static constexpr double kBase[3] = {2.16, 1.76, 1.30}, kStart[3] = {0.44, 0.78, 1.81}, kLine[3] = {0.320, 0.795, 1.663},
-                          kShare[3] = {0.743, 0.516, 1.108}, kRead[3] = {0.1125e-6, 0.100e-6, 0.107e-6};
+  static constexpr double kBase[3] = {2.14, 2.37, 1.42}, kStart[3] = {0.44, 0.0, 1.73}, kLine[3] = {0.354, 0.877, 1.711},
+                          kShare[3] = {0.706, 0.290, 0.970}, kRead[3] = {0.1085e-6, 0.115e-6, 0.111e-6};
   int64_t n = 0, tiles = 0;
   for (int i = 0; i < count; ++i) n += ns[i], tiles += ceil_div(ns[i], 256) * ceil_div(m, 256);
   for (int i = 0; i < 3; ++i) {
@@ -416,10 +416,10 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
   };
   const auto consider = [&](I8Plan p) {
     const int64_t pieces = p.whole > 0 ? (tiles - p.whole) * p.cut : (int64_t)p.nx * p.ny;
-    double us = 3.3 + (double)(n + m) * k * 0.072e-6 + rounds(p.whole, 256, 7.95, 0.340, 0.423, slices);
-    us += p.cut == 2 ? rounds((double)pieces, 256, 3.66, 0.282, 0.173, slices)
-                     : rounds((double)pieces * p.ks, 256, 2.23, 0.172, 0.0985, p.per);
-    if (p.ks > 1) us += 3.2 + 0.45e-6 * 4 * p.ks * m * n;
+    double us = 3.3 + (double)(n + m) * k * 0.072e-6 + rounds(p.whole, 256, 7.34, 0.351, 0.372, slices);
+    us += p.cut == 2 ? rounds((double)pieces, 256, 3.70, 0.304, 0.113, slices)
+                     : rounds((double)pieces * p.ks, 256, 1.87, 0.1845, 0.072, p.per);
+    if (p.ks > 1) us += 3.3 + 0.45e-6 * 4 * p.ks * m * n;
     if (us < least) least = us, best.skinny = 0, best.plan = p;
   };
   const int64_t rest = tiles % 256;
