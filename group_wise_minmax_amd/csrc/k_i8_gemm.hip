@@ -12,9 +12,9 @@
 //    and at 4.0 on random codes (32 x 32 x 32 shapes: 3.45, they take more power);
 //    m = 4096, n = 14336, k = 4096 200 us (2.4 POP/s; the library's product 217 to
 //    235), m = n = k = 8192 415 us, and 320 us with all codes 0.  Each wave takes
-//    128 x 64, so that its LDS reads (12 KiB for 32 MFMAs) fit under them; four
-//    waves of 128 x 128 needed more registers than there are without moving
-//    accumulators (337 us).
+//    128 x 64, so that its LDS reads (12 KiB for 32 MFMAs) fit under them (four
+//    waves of 128 x 128: 249 us where these took 247); loads are spread between
+//    the MFMAs (issued together 259 and 247).
 //  * pieces the operands: 80 to 92 bytes a ns come to a CU from L2 (m = 333, n = k
 //    = 8192 40.6 us).  Fewer LDS reads (64 x 64 a wave, two groups of waves that
 //    take a slice each) and operands read a whole step ahead gained nothing: 41.3
