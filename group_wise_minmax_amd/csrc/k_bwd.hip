@@ -202,15 +202,20 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
 #pragma unroll
     for (int b = 0; b < TM; ++b) acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  u32x4_t dr[DCH];
-  u32x4_t wraw;  // 32 codes of row 4q + lg (2-bit: dwords 0 and 1; 8-bit: the first 16)
-  u32x4_t wraw2;  // 8-bit: the last 16
-  float md_s;
-  int md_i;
-  float md_off = 0.f;  // the loaded stage's weight's offset (the binding may move on before the store)
-  int left = BNR;      // 8-bit: rows of the weight from the loaded stage on
+  // A stage on its way from memory.  r1: a second one (8-bit rows, below).
+  struct Raw {
+    u32x4_t dr[DCH];
+    u32x4_t wraw;   // 32 codes of row 4q + lg (2-bit: dwords 0 and 1; 8-bit: the first 16)
+    u32x4_t wraw2;  // 8-bit: the last 16
+    float md_s;
+    int md_i;
+    float md_off = 0.f;  // its weight's offset (the binding may move on before the store)
+    int left = BNR;      // 8-bit: rows of its weight from it on
+  };
+  Raw r0, r1;
   // loads of the stage starting at row vt of the set, from the bound weight
-  auto load_stage = [&](int64_t vt) {
+  auto load_stage = [&](int64_t vt, Raw& raw) {
+    auto& [dr, wraw, wraw2, md_s, md_i, md_off, left] = raw;
     const int st = (int)(vt / BNR);
     const Bound& b = cur;
     const __amdgpu_buffer_rsrc_t r_w = b.w, r_d = b.d, r_s = b.s, r_z = b.z;
@@ -254,7 +259,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
       md_s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r_s, g_voff * 4, go * 4, 0));
     }
   };
-  auto store_stage = [&](int buf) {
+  auto store_stage = [&](int buf, Raw& raw) {
+    auto& [dr, wraw, wraw2, md_s, md_i, md_off, left] = raw;
     char* ds = ds_base + buf * DS_BUF;
     if constexpr (T::fmt == FMT_INT8) {
       // dY past a token's last row is the next token's: cleared, so that an
@@ -357,11 +363,11 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
   // meet zero weights (buffer reads past the end) times finite dY values (8-bit
   // weights: times zeros, see store_stage).
   if constexpr (T::fmt == FMT_NF4) __syncthreads();  // pair table visible
-  load_stage(0);
-  store_stage(0);
+  load_stage(0, r0);
+  store_stage(0, r0);
   if (BNR < N) {
     bind_for(BNR);
-    load_stage(BNR);
+    load_stage(BNR, r0);
   }
   __syncthreads();
   int buf = 0;
@@ -382,8 +388,8 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
     auto stage = [&](int64_t t) {
       __builtin_amdgcn_s_setprio(1);
       if (t + BNR < N) {
-        store_stage(buf ^ 1);
-        if (t + 2 * BNR < N) load_stage(t + 2 * BNR);
+        store_stage(buf ^ 1, r0);
+        if (t + 2 * BNR < N) load_stage(t + 2 * BNR, r0);
       }
       __builtin_amdgcn_s_setprio(0);
     };
@@ -399,12 +405,90 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
       buf ^= 1;
     }
   } else {
-    for (int64_t nt = 0; nt < N; nt += BNR) {
+    int64_t nt = 0;
+    if constexpr (T::fmt == FMT_INT8 && TK == 4 && WGK * WGM == 8) {
+      // One phase a stage, in eight groups of TM MFMAs and a column of the next
+      // stage's weights each, so that a SIMD's two waves find work for the matrix
+      // core and the vector unit at once, and two stages on their way instead of one
+      // (a step takes about as long as a load).  m = 300, n = 4096, k = 14336: staged and
+      // multiplied one after the other 86.5 us, interleaved 82.5, with two stages
+      // 77.6; 2048 tokens through q, k and v of 8B 123.7, 124.3, 120.0.  (Not for 128 x
+      // 128 tiles of four waves: its registers leave no room for a second workgroup
+      // on a CU, and two rounds become three: m = 300, n = 4096, k = 14336 97 and 136 us.)
+      if (nt + 2 * BNR < N) {
+        bind_for(2 * BNR);
+        load_stage(2 * BNR, r1);
+      }
+      auto step = [&](int64_t nt, Raw& raw) {
+        auto& [dr, wraw, wraw2, md_s, md_i, md_off, left] = raw;
+        bind_for(nt + 3 * BNR);
+        const char* wt = wt_base + buf * WT_BUF;
+        const char* ds = ds_base + buf * DS_BUF;
+        char* wn = wt_base + (buf ^ 1) * WT_BUF;
+        char* dn = ds_base + (buf ^ 1) * DS_BUF;
+        u32x4_t af[2][TK], bf[2][TM];
+        auto read = [&](int h) {
+#pragma unroll
+          for (int a = 0; a < TK; ++a) af[h][a] = *reinterpret_cast<const u32x4_t*>(wt + (h ? a_base1 : a_base) + a * 16 * 128);
+#pragma unroll
+          for (int b = 0; b < TM; ++b) bf[h][b] = *reinterpret_cast<const u32x4_t*>(ds + (h ? b_base1 : b_base) + b * 16 * 128);
+        };
+        read(0);
+        const bool on = d_col < left;
+#pragma unroll
+        for (int i = 0; i < DCH; ++i) {
+          const int ci = tid + NT * i;
+          *reinterpret_cast<u32x4_t*>(dn + swz(ci >> 3, ci & 7)) = on ? dr[i] : u32x4_t{0u, 0u, 0u, 0u};
+        }
+        uint32_t wr[4] = {wraw[0], wraw[2], wraw2[0], wraw2[2]}, wr2[4] = {wraw[1], wraw[3], wraw2[1], wraw2[3]};
+        transpose_rows4(wr[0], wr[1], wr[2], wr[3]);
+        transpose_rows4(wr2[0], wr2[1], wr2[2], wr2[3]);
+        float sc[4];
+        gather_rows4(md_s, sc);
+        load_stage(nt + 3 * BNR, raw);
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int h = j / TK, a = j % TK;
+#pragma unroll
+          for (int b = 0; b < TM; ++b) acc[a][b] = mfma16x16x32(af[h][a], bf[h][b], acc[a][b]);
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = (float)(int)(int8_t)(uint8_t)((j < 4 ? wr[r] : wr2[r]) >> (8 * (j & 3))) * sc[r];
+          *reinterpret_cast<uint2*>(wn + swz(8 * c + j, q >> 1) + 8 * (q & 1)) =
+              make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+        buf ^= 1;
+      };
+      bool odd = false;
+      for (; nt + 4 * BNR < N; nt += 2 * BNR) {
+        step(nt, r0);
+        step(nt + BNR, r1);
+      }
+      // the last steps: stage nt + 1 in r0, nt + 2 in r1 (where they exist)
+      for (; nt < N; nt += BNR) {
+        if (nt + BNR < N) {
+          store_stage(buf ^ 1, odd ? r1 : r0);
+          if (nt + 3 * BNR < N) {
+            bind_for(nt + 3 * BNR);
+            load_stage(nt + 3 * BNR, odd ? r1 : r0);
+          }
+        }
+        compute(buf);
+        __syncthreads();
+        buf ^= 1;
+        odd = !odd;
+      }
+    }
+    for (; nt < N; nt += BNR) {
       if (nt + BNR < N) {
-        store_stage(buf ^ 1);
+        store_stage(buf ^ 1, r0);
         if (nt + 2 * BNR < N) {
           bind_for(nt + 2 * BNR);
-          load_stage(nt + 2 * BNR);
+          load_stage(nt + 2 * BNR, r0);
         }
       }
       compute(buf);

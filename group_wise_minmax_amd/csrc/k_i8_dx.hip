@@ -242,7 +242,7 @@ constexpr double kMostPart = 256e6;  // bytes of sums of a split reduction
 //    launch and the traffic of the sums.  (An estimate that went on linearly past
 //    one round chose 384 workgroups for 256 CUs: m = 40, n = 14336, k = 4096 34.8 us
 //    against 27.7 with four ranges.)
-//  * k_bwd_dx, per 64 rows: 0.713 a round of 128 x 128 tiles and 0.302, 1.32 a round
+//  * k_bwd_dx, per 64 rows: 0.713 a round of 128 x 128 tiles and 0.302, 1.20 a round
 //    of 256 x 128, 1.78 a round of 256 x 256.
 DxChoice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
   static constexpr double kBase[3] = {2.27, 2.25, 2.43}, kRound[3] = {1.31, 1.45, 1.84}, kSlice[3] = {0.0675, 0.075, 0.0955},
@@ -266,7 +266,7 @@ DxChoice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
   }
   const double stages = std::ceil(n / 64.0);
   const double t128 = 3.3 + stages * (0.713 * std::ceil(ceil_div(k, 128) * ceil_div(m, 128) / 256.0) + 0.302);
-  const double t256x128 = 4.2 + stages * 1.32 * std::ceil(ceil_div(k, 256) * ceil_div(m, 128) / 256.0);
+  const double t256x128 = 4.2 + stages * 1.20 * std::ceil(ceil_div(k, 256) * ceil_div(m, 128) / 256.0);
   const double t256 = 5.2 + stages * 1.78 * std::ceil(ceil_div(k, 256) * ceil_div(m, 256) / 256.0);
   if (t128 < least) least = t128, best = {0, 1, 0, 128, 128};
   if (t256x128 < least) least = t256x128, best = {0, 1, 0, 256, 128};
