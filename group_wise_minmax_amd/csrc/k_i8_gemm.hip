@@ -362,23 +362,34 @@ __global__ __launch_bounds__(256) void k_i8_reduce(I8Set set, const int* __restr
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a product of count weights of ns channels runs: by k_i8_skinny with tiles
-// of 16 * skinny (1, 2, 4), or (0) by k_i8_gemm as `plan` says.
+// of 16 tn channels and 16 tm tokens, or (tn 0) by k_i8_gemm as `plan` says.
 struct I8Choice {
-  int skinny;
+  int tn, tm;
   I8Plan plan;
 };
 
 // The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 700 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
-// cache): on these the choice is 1.8% off the best one on average.
-//  * k_i8_skinny: rounds of one workgroup a CU (T = 1: two, by their LDS), each
-//    at a rate for a 128-byte line of a wave that grows with the CUs at work.  (Its
-//    tokens are the grid's second dimension, which has 65535 workgroups.)
+// them on 1400 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
+// cache): on these the choice is 2.3% off the best one on average.
+//  * k_i8_skinny: rounds of workgroups, each at a rate for a 128-byte line of a wave
+//    that grows with the CUs at work.  (Its tokens are the grid's second dimension,
+//    which has 65535 workgroups.)
 //  * k_i8_gemm: the same with a rate for 64 of k: in 256 x 256 tiles whose last
 //    round is cut where it would leave half of the chip idle (128 x 256 pieces) or
 //    three quarters (128 x 128), or all in tiles or pieces of one size; 128 x 128
 //    pieces may split K, which costs a second launch and the traffic of the sums.
 constexpr int64_t kMostGridY = 65535;
+
+// Tiles of k_i8_skinny and what they cost (us): `base`, and a round of `room`
+// workgroups `start`, and for a 128-byte line of a wave `line` and, where all of the
+// room is taken, `share`; `read` for a byte of the weights.
+struct Skinny {
+  int tn, tm, room;
+  double base, start, line, share, read;
+};
+constexpr Skinny kSkinny[] = {{1, 1, 256, 2.38, 0.21, 0.401, 0.104, 0.110e-6}, {2, 1, 512, 2.33, 0.00, 0.615, 1.141, 0.122e-6},
+                              {4, 1, 256, 2.20, 0.00, 1.234, 0.344, 0.147e-6}, {2, 2, 256, 2.40, 0.00, 0.832, 0.356, 0.110e-6},
+                              {4, 2, 256, 1.51, 0.89, 1.288, 0.733, 0.131e-6}, {4, 4, 256, 1.28, 1.94, 1.599, 1.025, 0.109e-6}};
 
 I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
   // us of `groups` workgroups, `room` of them at a time: each costs `steps` steps
@@ -389,21 +400,18 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
     if (r > full) us += start + steps * (step + share * (r - full));
     return us;
   };
-  I8Choice best{1, {}};
+  I8Choice best{};
   double least = 1e30;
-  static constexpr double kBase[3] = {2.14, 2.37, 1.42}, kStart[3] = {0.44, 0.0, 1.73}, kLine[3] = {0.354, 0.877, 1.711},
-                          kShare[3] = {0.706, 0.290, 0.970}, kRead[3] = {0.1085e-6, 0.115e-6, 0.111e-6};
   int64_t n = 0, tiles = 0;
   for (int i = 0; i < count; ++i) n += ns[i], tiles += ceil_div(ns[i], 256) * ceil_div(m, 256);
-  for (int i = 0; i < 3; ++i) {
-    const int t = 1 << i;
+  for (const Skinny& c : kSkinny) {
     int64_t groups = 0;
-    if (ceil_div(m, 16 * t) > kMostGridY) continue;
-    for (int j = 0; j < count; ++j) groups += ceil_div(ns[j], 16 * t);
-    groups *= ceil_div(m, 16 * t);
-    const double us = kBase[i] + rounds((double)groups, t == 1 ? 512 : 256, kStart[i], kLine[i], kShare[i], (double)ceil_div(k, 1024)) +
-                      kRead[i] * (double)n * k;
-    if (us < least) least = us, best.skinny = t;
+    if (ceil_div(m, 16 * c.tm) > kMostGridY) continue;
+    for (int j = 0; j < count; ++j) groups += ceil_div(ns[j], 16 * c.tn);
+    groups *= ceil_div(m, 16 * c.tm);
+    const double us = c.base + rounds((double)groups, c.room, c.start, c.line, c.share, (double)ceil_div(k, 1024)) +
+                      c.read * (double)n * k;
+    if (us < least) least = us, best.tn = c.tn, best.tm = c.tm;
   }
   const int slices = (int)(k / I8K);
   const auto plan = [&](int64_t whole, int cut) {
@@ -416,11 +424,11 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
   };
   const auto consider = [&](I8Plan p) {
     const int64_t pieces = p.whole > 0 ? (tiles - p.whole) * p.cut : (int64_t)p.nx * p.ny;
-    double us = 3.3 + (double)(n + m) * k * 0.072e-6 + rounds(p.whole, 256, 7.34, 0.351, 0.372, slices);
-    us += p.cut == 2 ? rounds((double)pieces, 256, 3.70, 0.304, 0.113, slices)
-                     : rounds((double)pieces * p.ks, 256, 1.87, 0.1845, 0.072, p.per);
-    if (p.ks > 1) us += 3.3 + 0.45e-6 * 4 * p.ks * m * n;
-    if (us < least) least = us, best.skinny = 0, best.plan = p;
+    double us = 3.1 + (double)(n + m) * k * 0.070e-6 + rounds(p.whole, 256, 8.19, 0.357, 0.349, slices);
+    us += p.cut == 2 ? rounds((double)pieces, 256, 3.69, 0.309, 0.124, slices)
+                     : rounds((double)pieces * p.ks, 256, 1.96, 0.183, 0.078, p.per);
+    if (p.ks > 1) us += 3.4 + 0.44e-6 * 4 * p.ks * m * n;
+    if (us < least) least = us, best = {0, 0, p};
   };
   const int64_t rest = tiles % 256;
   if (tiles > 256 && rest > 0 && rest <= 128) consider(plan(tiles - rest, rest <= 64 ? 4 : 2));
@@ -439,7 +447,7 @@ I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) 
 }  // namespace
 
 static size_t part_bytes(const I8Choice& c, const int64_t* ns, int count, int64_t m) {
-  if (c.skinny != 0 || c.plan.ks == 1) return 0;
+  if (c.tn != 0 || c.plan.ks == 1) return 0;
   int64_t n = 0;
   for (int i = 0; i < count; ++i) n += padded((int)ns[i]);
   return (size_t)c.plan.ks * (size_t)m * (size_t)n * sizeof(int);
@@ -477,7 +485,7 @@ hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs
   }
   I8Choice c = choose(ns, set.count, k, m, true);
   if (part_bytes(c, ns, set.count, m) > work_bytes) c = choose(ns, set.count, k, m, false);
-  if (c.skinny != 0) return launch_i8_skinny(set, c.skinny, Xq, xs, m, k, lora, s);
+  if (c.tn != 0) return launch_i8_skinny(set, c.tn, c.tm, Xq, xs, m, k, lora, s);
   const I8Plan& plan = c.plan;
   for (int i = 0; i < set.count; ++i) set.tile_end[i] = end += (int)ceil_div(set.n[i], plan.whole > 0 ? 256 : 128);
   int* part = plan.ks > 1 ? static_cast<int*>(work) : nullptr;

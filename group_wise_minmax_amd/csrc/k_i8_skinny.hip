@@ -2,7 +2,9 @@
 // (the weight is streamed from memory once and bounds the time) and small
 // weights at longer ones (too few 256 x 256 tiles to fill the chip).
 //
-// A workgroup computes 16 T channels of 16 T tokens (T = 1, 2 or 4).  Its eight
+// A workgroup computes 16 TN channels of 16 TM tokens (1, 2 or 4; more channels than
+// tokens where the tokens are few and would be fetched for every 16 channels again:
+// m = 12, n = 14336, k = 4096 17.6 us with 32 x 32, 16.4 with 64 x 16).  Its eight
 // waves split K among them, a 128-byte line of every row by turns; each wave
 // loads its share straight to LDS into a ring of its own, so that it waits
 // for its own loads only and no barrier is needed, and multiplies it on
@@ -56,21 +58,21 @@ __device__ __forceinline__ void barrier_lds() {
   asm volatile("" ::: "memory");
 }
 
-// U slots of a ring: with two for T = 2 a CU has room for two workgroups (m = 24, n =
-// 14336, k = 4096, 448 workgroups: four slots 19.9 us, two 18.9); T = 1 gains nothing
-// from fewer (16.2 and 16.5 us at m = 5).
-template <int T, int U>
+// U slots of a ring: with two for 32 x 32 a CU has room for two workgroups (m = 24, n
+// = 14336, k = 4096, 448 workgroups: four slots 19.9 us, two 18.9); 16 x 16 gains
+// nothing from fewer (16.2 and 16.5 us at m = 5).
+template <int TN, int TM, int U>
 __global__ __launch_bounds__(kThreads) void k_i8_skinny(I8Set set, const int8_t* __restrict__ Xq,
                                                        const float* __restrict__ xs, int m, int k, LoraEpi lora) {
-  static_assert(U * 2 * T >= T * T, "a wave's sums fit its ring");
-  __shared__ __attribute__((aligned(1024))) int8_t ring[kWaves][U][2 * T * 1024];
+  static_assert(U * (TN + TM) >= TN * TM, "a wave's sums fit its ring");
+  __shared__ __attribute__((aligned(1024))) int8_t ring[kWaves][U][(TN + TM) * 1024];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // the same in the wave: scalar load offsets
   const int li = lane & 15, lg = lane >> 4;
   int tile = blockIdx.x;
   const int wi = weight_of(set, tile);
   const int n = set.n[wi];
-  const int n0 = tile * 16 * T, m0 = blockIdx.y * 16 * T;
+  const int n0 = tile * 16 * TN, m0 = blockIdx.y * 16 * TM;
 
   // A load fills 16 rows of 64 bytes: lane l the 16 bytes at position l % 4 of
   // row l / 4.  Rows past the end load the last row instead (their outputs are
@@ -78,55 +80,55 @@ __global__ __launch_bounds__(kThreads) void k_i8_skinny(I8Set set, const int8_t*
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(set.w[wi], (int64_t)n * k);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(Xq, (int64_t)m * k);
   const int lr = lane >> 2, lc = 16 * ((lane & 3) ^ i8_key(lr));
-  int ow[T], ox[T];
+  int ow[TN], ox[TM];
 #pragma unroll
-  for (int a = 0; a < T; ++a) ow[a] = min(n0 + 16 * a + lr, n - 1) * k + lc;
+  for (int a = 0; a < TN; ++a) ow[a] = min(n0 + 16 * a + lr, n - 1) * k + lc;
 #pragma unroll
-  for (int b = 0; b < T; ++b) ox[b] = min(m0 + 16 * b + lr, m - 1) * k + lc;
+  for (int b = 0; b < TM; ++b) ox[b] = min(m0 + 16 * b + lr, m - 1) * k + lc;
   auto load = [&](int u, int j) {
     const int kt = slice_at(wave, j);
 #pragma unroll
-    for (int a = 0; a < T; ++a) load_to_lds(rw, &ring[wave][u][1024 * a], ow[a], kt);
+    for (int a = 0; a < TN; ++a) load_to_lds(rw, &ring[wave][u][1024 * a], ow[a], kt);
 #pragma unroll
-    for (int b = 0; b < T; ++b) load_to_lds(rx, &ring[wave][u][1024 * (T + b)], ox[b], kt);
+    for (int b = 0; b < TM; ++b) load_to_lds(rx, &ring[wave][u][1024 * (TN + b)], ox[b], kt);
   };
   const int cnt = slices_of(wave, k);
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (u < cnt) load(u, u);
 
-  i32x4_t acc[T][T];
+  i32x4_t acc[TN][TM];
 #pragma unroll
-  for (int a = 0; a < T; ++a)
+  for (int a = 0; a < TN; ++a)
 #pragma unroll
-    for (int b = 0; b < T; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
+    for (int b = 0; b < TM; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
   const int f = li * 64 + 16 * (lg ^ i8_key(li));
-  run_ring<U, 2 * T>(cnt, load, [&](int u, int) {
-    i32x4_t w[T], x[T];
+  run_ring<U, TN + TM>(cnt, load, [&](int u, int) {
+    i32x4_t w[TN], x[TM];
 #pragma unroll
-    for (int a = 0; a < T; ++a) w[a] = *reinterpret_cast<const i32x4_t*>(&ring[wave][u][1024 * a + f]);
+    for (int a = 0; a < TN; ++a) w[a] = *reinterpret_cast<const i32x4_t*>(&ring[wave][u][1024 * a + f]);
 #pragma unroll
-    for (int b = 0; b < T; ++b) x[b] = *reinterpret_cast<const i32x4_t*>(&ring[wave][u][1024 * (T + b) + f]);
+    for (int b = 0; b < TM; ++b) x[b] = *reinterpret_cast<const i32x4_t*>(&ring[wave][u][1024 * (TN + b) + f]);
 #pragma unroll
-    for (int a = 0; a < T; ++a)
+    for (int a = 0; a < TN; ++a)
 #pragma unroll
-      for (int b = 0; b < T; ++b) acc[a][b] = mfma_i8(w[a], x[b], acc[a][b]);
+      for (int b = 0; b < TM; ++b) acc[a][b] = mfma_i8(w[a], x[b], acc[a][b]);
   });
 
   // The waves' sums, each in its own ring, then added.
   i32x4_t* const sums = reinterpret_cast<i32x4_t*>(&ring[wave][0][0]);
 #pragma unroll
-  for (int a = 0; a < T; ++a)
+  for (int a = 0; a < TN; ++a)
 #pragma unroll
-    for (int b = 0; b < T; ++b) sums[(a * T + b) * 64 + lane] = acc[a][b];
+    for (int b = 0; b < TM; ++b) sums[(a * TM + b) * 64 + lane] = acc[a][b];
   __syncthreads();
   // Channels n = 4 (lane / 16) + i of token lane % 16, a block a wave by turns.
-  for (int blk = wave; blk < T * T; blk += kWaves) {
+  for (int blk = wave; blk < TN * TM; blk += kWaves) {
     i32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const i32x4_t*>(&ring[w][0][0])[blk * 64 + lane];
-    const int mr = m0 + (blk % T) * 16 + li;
-    i8_store(set, wi, mr < m ? xs[mr] : 0.f, v, mr, m, n0 + (blk / T) * 16, lora);
+    const int mr = m0 + (blk % TM) * 16 + li;
+    i8_store(set, wi, mr < m ? xs[mr] : 0.f, v, mr, m, n0 + (blk / TM) * 16, lora);
   }
 }
 
@@ -225,21 +227,27 @@ unsigned tile_rows(I8Set& set, int t) {
   return (unsigned)end;
 }
 
-template <int T, int U>
+template <int TN, int TM, int U>
 hipError_t launch(I8Set set, const int8_t* Xq, const float* xs, int64_t m, int64_t k, const LoraEpi& lora, hipStream_t s) {
-  const unsigned rows = tile_rows(set, T);
-  hipLaunchKernelGGL((k_i8_skinny<T, U>), dim3(rows, (unsigned)((m + 16 * T - 1) / (16 * T))), dim3(kThreads), 0, s, set,
-                     Xq, xs, (int)m, (int)k, lora);
+  const unsigned rows = tile_rows(set, TN);
+  hipLaunchKernelGGL((k_i8_skinny<TN, TM, U>), dim3(rows, (unsigned)((m + 16 * TM - 1) / (16 * TM))), dim3(kThreads), 0, s,
+                     set, Xq, xs, (int)m, (int)k, lora);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_i8_skinny(const I8Set& set, int t, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
+hipError_t launch_i8_skinny(const I8Set& set, int tn, int tm, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
                             const LoraEpi& lora, hipStream_t s) {
-  if (t == 1) return launch<1, 4>(set, Xq, xs, m, k, lora, s);
-  if (t == 2) return launch<2, 2>(set, Xq, xs, m, k, lora, s);
-  return launch<4, 2>(set, Xq, xs, m, k, lora, s);
+  switch (8 * tn + tm) {
+    case 8 * 1 + 1: return launch<1, 1, 4>(set, Xq, xs, m, k, lora, s);
+    case 8 * 2 + 1: return launch<2, 1, 2>(set, Xq, xs, m, k, lora, s);
+    case 8 * 4 + 1: return launch<4, 1, 2>(set, Xq, xs, m, k, lora, s);
+    case 8 * 2 + 2: return launch<2, 2, 2>(set, Xq, xs, m, k, lora, s);
+    case 8 * 4 + 2: return launch<4, 2, 2>(set, Xq, xs, m, k, lora, s);
+    case 8 * 4 + 4: return launch<4, 4, 2>(set, Xq, xs, m, k, lora, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_i8_decode(const I8Set& weights, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora,

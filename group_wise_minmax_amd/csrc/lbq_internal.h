@@ -210,9 +210,9 @@ I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const in
 size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m);
 hipError_t launch_i8_fwd(const I8Set& set, const int8_t* Xq, const float* xs, int64_t m, int64_t k, const LoraEpi& lora,
                          void* work, size_t work_bytes, hipStream_t s);
-// The same by workgroups of 16 t channels and 16 t tokens (t = 1, 2, 4) that
-// split K over their waves; set.tile_end is not looked at.
-hipError_t launch_i8_skinny(const I8Set& set, int t, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
+// The same by workgroups of 16 tn channels and 16 tm tokens (1, 2 or 4, tm <= tn)
+// that split K over their waves; set.tile_end is not looked at.
+hipError_t launch_i8_skinny(const I8Set& set, int tn, int tm, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
                             const LoraEpi& lora, hipStream_t s);
 // From bf16 tokens X [m][k] in one launch: m <= 4 and m * k <= kI8DecodeCodes.
 constexpr int kI8DecodeCodes = 16384;

@@ -161,6 +161,15 @@ def test_forward_bitexact(L, n, k):
         bits_equal(L.lbq_linear_fwd_tokens(codes, scales, qw), want)
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 8200, 1024), (12, 14336, 1024), (13, 5001, 2048), (16, 28672, 512), (24, 14336, 1088),
+                                   (30, 4100, 4096), (48, 9001, 1024), (64, 14336, 512), (90, 4096, 2048)])
+def test_forward_of_few_tokens_through_many_channels(L, m, n, k):
+    """Every tile shape of the short products: 16 to 64 channels by 16 to 64 tokens."""
+    qw, (wq, ws) = weight(L, 8, n, k)
+    x = tokens(m, m, k)
+    bits_equal(L.lbq_linear_fwd(to_dev_bf16(x), qw), I8.product_bf16(*I8.tokens(x), wq, ws))
+
+
 @pytest.mark.parametrize("m", [0, 1, 2, 5, 64, 130])
 def test_forward_leaves_the_rest_alone(L, m):
     """A strided output, and guard rows before and after it; m = 0 writes nothing."""
