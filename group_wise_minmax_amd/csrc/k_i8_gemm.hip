@@ -368,16 +368,6 @@ struct I8Choice {
   I8Plan plan;
 };
 
-// The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 1400 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
-// cache): on these the choice is 2.3% off the best one on average.
-//  * k_i8_skinny: rounds of workgroups, each at a rate for a 128-byte line of a wave
-//    that grows with the CUs at work.  (Its tokens are the grid's second dimension,
-//    which has 65535 workgroups.)
-//  * k_i8_gemm: the same with a rate for 64 of k: in 256 x 256 tiles whose last
-//    round is cut where it would leave half of the chip idle (128 x 256 pieces) or
-//    three quarters (128 x 128), or all in tiles or pieces of one size; 128 x 128
-//    pieces may split K, which costs a second launch and the traffic of the sums.
 constexpr int64_t kMostGridY = 65535;
 
 // Tiles of k_i8_skinny and what they cost (us): `base`, and a round of `room`
@@ -391,6 +381,16 @@ constexpr Skinny kSkinny[] = {{1, 1, 256, 2.38, 0.21, 0.401, 0.104, 0.110e-6}, {
                               {4, 1, 256, 2.20, 0.00, 1.234, 0.344, 0.147e-6}, {2, 2, 256, 2.40, 0.00, 0.832, 0.356, 0.110e-6},
                               {4, 2, 256, 1.51, 0.89, 1.288, 0.733, 0.131e-6}, {4, 4, 256, 1.28, 1.94, 1.599, 1.025, 0.109e-6}};
 
+// The cheapest by an estimate in microseconds, fitted to the times of all of
+// them on 1400 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
+// cache): on these the choice is 2.3% off the best one on average.
+//  * k_i8_skinny: rounds of workgroups, each at a rate for a 128-byte line of a wave
+//    that grows with the CUs at work.  (Its tokens are the grid's second dimension,
+//    which has 65535 workgroups.)
+//  * k_i8_gemm: the same with a rate for 64 of k: in 256 x 256 tiles whose last
+//    round is cut where it would leave half of the chip idle (128 x 256 pieces) or
+//    three quarters (128 x 128), or all in tiles or pieces of one size; 128 x 128
+//    pieces may split K, which costs a second launch and the traffic of the sums.
 I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
   // us of `groups` workgroups, `room` of them at a time: each costs `steps` steps
   // of `step` and `share` where all of the room is taken
