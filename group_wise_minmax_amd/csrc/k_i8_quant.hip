@@ -76,7 +76,7 @@ __global__ __launch_bounds__(NT) void k_i8_quant_rows(const T* __restrict__ X, i
     if (t.part == nullptr || tid >= t.rp) return;
     const int64_t tr = row0 + row;
     float v = 0.f;
-    if (tid < t.r) v = t.sigma * sum_splits(t.part, t.splits, t.m * t.rb, tr * t.rb + tid);
+    if (tid < t.r) v = t.sigma * sum_splits16(t.part, t.splits, t.m * t.rb, tr * t.rb + tid);
     t.T[tr * t.rp + tid] = (uint16_t)bf16_rne(v);
   };
   if constexpr (KEEP) {

@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void k_i8_decode(I8Set set, const uint16_
   if (t.part != nullptr && tid < m * t.rp) {
     const int r = tid / t.rp, j = tid % t.rp;
     float v = 0.f;
-    if (j < t.r) v = t.sigma * sum_splits(t.part, t.splits, t.m * t.rb, (int64_t)r * t.rb + j);
+    if (j < t.r) v = t.sigma * sum_splits16(t.part, t.splits, t.m * t.rb, (int64_t)r * t.rb + j);
     T[tid] = (uint16_t)bf16_rne(v);
   }
   uint32_t mx = 0;

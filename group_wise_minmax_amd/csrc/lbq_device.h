@@ -401,6 +401,21 @@ __device__ __forceinline__ float sum_splits(const float* __restrict__ part, int 
   return v;
 }
 
+// The same sum, bit for bit, for few threads that have nothing else to hide the
+// loads behind: sixteen in flight (absent ones add +0 to a sum that is never -0;
+// m = 64, n = 4096, k = 14336, rank 16 38.1 us with four, 36.3 with these).
+__device__ __forceinline__ float sum_splits16(const float* __restrict__ part, int splits, int64_t stride, int64_t off) {
+  float v = 0.f;
+  for (int s = 0; s < splits; s += 16) {
+    float p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = s + i < splits ? part[(s + i) * stride + off] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += p[i];
+  }
+  return v;
+}
+
 // bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
 __device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
 
