@@ -535,6 +535,39 @@ def test_lora_forward(L, n, k, r):
         assert (np.abs(y - ref) <= tol).all(), np.max(np.abs(y - ref) / tol)
 
 
+@pytest.mark.parametrize("m", [1, 6, 300])
+def test_lora_forward_replayed_and_on_two_streams(L, m):
+    """A captured adapted layer replayed with new tokens beside eager calls, and two
+    layers on two streams at once: the bits of the calls alone."""
+    n, k, r = 520, 1088, 24
+    qws = [weight(L, 96 + i, n, k)[0] for i in range(2)]
+    parts = [tuple(map(to_dev_bf16, lora_parts(20 + i, n, k, r))) for i in range(2)]
+    x = to_dev_bf16(tokens(1, m, k))
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        L.lbq_lora_fwd(x, qws[0], *parts[0], 0.5, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.lbq_lora_fwd(x, qws[0], *parts[0], 0.5, out=y)
+    for turn in range(4):
+        x.copy_(to_dev_bf16(tokens(30 + turn, m, k)))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, L.lbq_lora_fwd(x, qws[0], *parts[0], 0.5))
+    want = [L.lbq_lora_fwd(x, q, *p, 0.5) for q, p in zip(qws, parts)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for turn in range(8):
+        with torch.cuda.stream(streams[turn % 2]):
+            got.append(L.lbq_lora_fwd(x, qws[turn % 2], *parts[turn % 2], 0.5))
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[i % 2]) for i, v in enumerate(got))
+
+
 def test_lora_backward(L):
     n, k, r, m, sigma = 128, 320, 16, 45, 2.0
     qw, (q, s) = weight(L, 95, n, k)
