@@ -864,12 +864,15 @@ lbq_status lbq_lora_fwd(const lbq_desc* desc, const lbq_qtensor* q, const uint16
 static lbq_status check_grads(int32_t count, const lbq_grad* g, bool write) {
   if (count < 1) return fail(LBQ_E_SHAPE, "count must be at least 1 (got %d)", count);
   if (g == nullptr) return fail(LBQ_E_NULL, "grads must be non-NULL");
+  constexpr int64_t kMost = int64_t(1) << 40;  // values of all the tensors
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (g[i].dtype != LBQ_F32 && g[i].dtype != LBQ_BF16 && g[i].dtype != LBQ_F16)
       return fail(LBQ_E_FORMAT, "grads[%d].dtype must be 0 (fp32), 1 (bf16) or 2 (fp16), got %d", i, g[i].dtype);
-    if (g[i].numel < 0 || (total += g[i].numel) > (int64_t(1) << 40))
-      return fail(LBQ_E_SHAPE, "numel must be at least 0 and 2^40 in all (grads[%d] has %lld)", i, (long long)g[i].numel);
+    if (g[i].numel < 0 || g[i].numel > kMost - total)
+      return fail(LBQ_E_SHAPE, "numel must be at least 0, and at most 2^40 in all (grads[%d] has %lld)", i,
+                  (long long)g[i].numel);
+    total += g[i].numel;
     if (g[i].numel == 0) continue;
     const size_t size = g[i].dtype == LBQ_F32 ? 4 : 2;
     if (g[i].grad == nullptr || (write && g[i].out == nullptr))

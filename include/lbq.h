@@ -406,8 +406,9 @@ typedef enum { LBQ_NORM_2 = 0, LBQ_NORM_INF = 1 } lbq_norm;
 /* One gradient tensor: `numel` contiguous values of type lbq_dtype at `grad`
  * (device), and where lbq_clip_grads writes them scaled: `out`, of the same
  * type, the same pointer as `grad` (in place) or memory of its own.  Both are
- * aligned to the type (16-byte aligned tensors run faster).  numel >= 0, at
- * most 2^40; with numel 0 the pointers are not looked at. */
+ * aligned to the type (16-byte aligned tensors run faster).  numel >= 0, and at
+ * most 2^40 in all the tensors of a call (LBQ_E_SHAPE otherwise); with numel 0
+ * the pointers are not looked at. */
 typedef struct {
   const void* grad;
   void* out;
@@ -416,7 +417,8 @@ typedef struct {
   int32_t reserved; /* 0 */
 } lbq_grad;
 
-/* Workspace bytes the two calls below take. */
+/* Workspace bytes the two calls below take (0 as well for a list that they
+ * refuse). */
 size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads);
 
 /* Norm over all the values of `count` tensors (count >= 1; a tensor listed

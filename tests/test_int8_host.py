@@ -304,3 +304,18 @@ def test_python_refusals_without_a_device(L):
         L.lbq_quantize_tokens(torch.zeros(4, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         L.make_desc("int7", 64, 64)
+
+
+@pytest.mark.parametrize("numels", [
+    (8, (1 << 63) - 1), ((1 << 63) - 1, 8), (1 << 39, 1 << 39, 1), (8, (1 << 63) - 8, 8), ((1 << 40) + 1,), (8, -1),
+    ((1 << 40), (1 << 63) - 1, (1 << 63) - 1),
+])
+def test_sizes_of_gradients_are_bounded_in_all(L, numels):
+    """More than 2^40 values over all the tensors, also where their sum passes 64 bits."""
+    t = grads_of(L, *[(A, A + (1 << 44) * (i + 1), n, 0) for i, n in enumerate(numels)])
+    far = A - (1 << 20)
+    assert L.lib.lbq_grad_workspace_bytes(len(numels), t) == 0
+    assert status(L, L.lib.lbq_grad_norm(len(numels), t, 0, far, far + 64, 1 << 18, None)) == "LBQ_E_SHAPE"
+    assert status(L, L.lib.lbq_clip_grads(len(numels), t, 0, 1.0, far, far + 64, 1 << 18, None)) == "LBQ_E_SHAPE"
+    full = grads_of(L, *[(A, A, 1 << 39, 0)] * 2)
+    assert L.lib.lbq_grad_workspace_bytes(2, full) == 8 * 2048
