@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 from dataclasses import dataclass, field
 from typing import Optional
 
@@ -606,13 +607,15 @@ def lbq_linear_fwd_tokens(codes: torch.Tensor, scales: torch.Tensor, qw: Quantiz
 
 _GRAD_DTYPE = {torch.float32: LBQ_F32, torch.bfloat16: LBQ_BF16, torch.float16: LBQ_F16}
 _NORM_TYPE = {2.0: LBQ_NORM_2, float("inf"): LBQ_NORM_INF}
+# What a table entry says of a tensor.
+_ENTRY = (torch.Tensor.data_ptr, torch.Tensor.numel, operator.attrgetter("dtype"), torch.Tensor.is_contiguous)
 
 
 class LbqGradSet:
     """The gradient tensors of one training step, for their norm and clipping
     (see ``lbq_grad_norm`` and ``lbq_clip_grads`` in lbq.h).  A program whose
     gradient buffers live as long as the training run builds it once; a tensor
-    whose storage moved is looked up again at the next call.
+    whose storage, type or layout changed is looked up (or refused) at the next call.
 
     ``grads``: contiguous fp32, bf16 or fp16 tensors on one device.  ``outs``:
     where ``clip`` writes the scaled gradients (tensors of the same types and
@@ -633,12 +636,12 @@ class LbqGradSet:
         self._look()
 
     def _look(self) -> None:
-        """Fill the table from the tensors, unless all are where they were."""
-        seen = [t.data_ptr() for t in self._grads]
-        seen += [t.numel() for t in self._grads]
-        if self._outs is not self._grads:
-            seen += [t.data_ptr() for t in self._outs]
-            seen += [t.numel() for t in self._outs]
+        """Fill the table from the tensors, unless all are as they were: another
+        view's values may begin at the same address and be as many."""
+        seen = []
+        for ts in (self._grads,) if self._outs is self._grads else (self._grads, self._outs):
+            for what in _ENTRY:
+                seen += map(what, ts)
         if seen == self._seen:
             return
         for i, (g, o) in enumerate(zip(self._grads, self._outs)):

@@ -228,3 +228,30 @@ def test_refusals(L):
     with pytest.raises(ValueError):
         L.LbqGradSet([g], [])
     assert torch.equal(g, torch.ones(10, device=DEV))
+
+
+def test_set_follows_tensors_that_change_type_or_layout(L):
+    """A view of another type or stride that begins where the tensor did and has as
+    many values: scaled as what it is, or refused, and nothing beside it is written."""
+    buf = made([200], TYPES[:1], 3)[0]
+    keep = buf.clone()
+    g = buf[:100]
+    s = L.LbqGradSet([g])
+    g.data = buf.view(torch.bfloat16)[:100]
+    before = wide([g])
+    want = I8.grad_norm(before)
+    assert abs(float(s.clip(0.5 * want)) - want) <= 2 ** -23 * want
+    c = I8.clip_factor(want, 0.5 * want)
+    tol = (HALF[torch.bfloat16] + 6 * 2 ** -24) * np.abs(before[0] * c) + TINY[torch.bfloat16]
+    assert (np.abs(wide([g])[0] - before[0] * c) <= tol).all()
+    assert torch.equal(buf[50:], keep[50:])
+    keep = buf.clone()
+    g.data = buf[::2]
+    for call in (s.norm, lambda: s.clip(1e-3)):
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(buf.view(torch.int32), keep.view(torch.int32))
+    g.data = buf[100:]
+    assert abs(float(s.norm()) - I8.grad_norm(wide([buf[100:]]))) <= 1e-6
+'''

@@ -319,3 +319,54 @@ def test_sizes_of_gradients_are_bounded_in_all(L, numels):
     assert status(L, L.lib.lbq_clip_grads(len(numels), t, 0, 1.0, far, far + 64, 1 << 18, None)) == "LBQ_E_SHAPE"
     full = grads_of(L, *[(A, A, 1 << 39, 0)] * 2)
     assert L.lib.lbq_grad_workspace_bytes(2, full) == 8 * 2048
+
+
+def host_set(L, grads, outs=None):
+    """A set of CPU tensors, for its table alone (no call takes it)."""
+    s = object.__new__(L.LbqGradSet)
+    s._grads, s._outs, s.device = grads, grads if outs is None else outs, grads[0].device
+    s._table, s._seen = (L.Grad * len(grads))(), None
+    s._look()
+    return s
+
+
+def entries(s):
+    return [(e.grad, e.out, e.numel, e.dtype) for e in s._table]
+
+
+@pytest.mark.parametrize("place", ["grads", "outs"])
+def test_set_sees_another_type_at_the_same_address(L, place):
+    """As many bf16 values at the address of fp32 ones, and fp16 seen as bf16."""
+    import torch
+    for first, view, code in ((torch.float32, torch.bfloat16, 1), (torch.float16, torch.bfloat16, 1), (torch.float32, torch.float16, 2)):
+        g, o = torch.zeros(100, dtype=first), torch.zeros(100, dtype=first)
+        s = host_set(L, [g], [o])
+        moved = g if place == "grads" else o
+        moved.data = moved.data.view(view)[:100]
+        with pytest.raises(ValueError):  # the other one is still of the first type
+            s._look()
+        s = host_set(L, [g := torch.zeros(100, dtype=first)])
+        g.data = g.data.view(view)[:100]
+        s._look()
+        assert entries(s) == [(g.data_ptr(), g.data_ptr(), 100, code)]
+        g.data = torch.zeros(100, dtype=torch.float64)
+        with pytest.raises(ValueError):
+            s._look()
+
+
+@pytest.mark.parametrize("place", ["grads", "outs"])
+def test_set_refuses_a_strided_view_at_the_same_address(L, place):
+    import torch
+    bufs = [torch.zeros(200), torch.zeros(200)]
+    g, o = bufs[0][:100], bufs[1][:100]
+    s = host_set(L, [g], [o])
+    moved, buf = (g, bufs[0]) if place == "grads" else (o, bufs[1])
+    moved.data = buf[::2]
+    assert moved.numel() == 100 and moved.data_ptr() == buf.data_ptr()
+    with pytest.raises(ValueError):
+        s._look()
+    m = torch.zeros(10, 10)
+    s = host_set(L, [m])
+    m.t_()
+    with pytest.raises(ValueError):
+        s._look()
