@@ -644,6 +644,7 @@ class LbqGradSet:
                 seen += map(what, ts)
         if seen == self._seen:
             return
+        self._seen = None  # a refusal below leaves a table that is filled again
         for i, (g, o) in enumerate(zip(self._grads, self._outs)):
             if g.dtype not in _GRAD_DTYPE or not g.is_contiguous() or g.device != self.device:
                 raise ValueError(f"grads[{i}] must be a contiguous fp32, bf16 or fp16 tensor on {self.device}")

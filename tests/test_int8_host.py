@@ -370,3 +370,19 @@ def test_set_refuses_a_strided_view_at_the_same_address(L, place):
     m.t_()
     with pytest.raises(ValueError):
         s._look()
+
+
+def test_set_fills_its_table_again_after_a_refusal(L):
+    """A first tensor that moved beside a second one that is refused; both back in
+    their places the table is that of the first look."""
+    import torch
+    a, b = torch.zeros(50), torch.zeros(60)
+    at, bt = a.data, b.data
+    s = host_set(L, [a, b])
+    want = entries(s)
+    a.data, b.data = torch.zeros(70), torch.zeros(120)[::2]
+    with pytest.raises(ValueError):
+        s._look()
+    a.data, b.data = at, bt
+    s._look()
+    assert entries(s) == want
