@@ -254,4 +254,3 @@ def test_set_follows_tensors_that_change_type_or_layout(L):
     assert torch.equal(buf.view(torch.int32), keep.view(torch.int32))
     g.data = buf[100:]
     assert abs(float(s.norm()) - I8.grad_norm(wide([buf[100:]]))) <= 1e-6
-'''
