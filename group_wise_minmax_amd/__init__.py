@@ -616,6 +616,10 @@ class LbqGradSet:
     (see ``lbq_grad_norm`` and ``lbq_clip_grads`` in lbq.h).  A program whose
     gradient buffers live as long as the training run builds it once; a tensor
     whose storage, type or layout changed is looked up (or refused) at the next call.
+    The set holds the tensors themselves, not the parameters they belong to: after
+    ``optimizer.zero_grad(set_to_none=True)``, torch's default, the next backward
+    makes new ones and the set would go on scaling the old.  Such a loop calls
+    ``lbq_clip_grad_norm_`` with the present gradients, or ``zero_grad(set_to_none=False)``.
 
     ``grads``: contiguous fp32, bf16 or fp16 tensors on one device.  ``outs``:
     where ``clip`` writes the scaled gradients (tensors of the same types and
@@ -688,5 +692,6 @@ def lbq_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
 
 def lbq_clip_grad_norm_(grads, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
     """Scale ``grads`` in place so that their norm over all the values is at
-    most ``max_norm``; returns the norm before that."""
+    most ``max_norm``; returns the norm before that.  The list is looked up at
+    every call: the form for gradients that each step makes anew."""
     return LbqGradSet(grads).clip(max_norm, norm_type)

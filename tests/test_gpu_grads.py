@@ -233,7 +233,7 @@ def test_refusals(L):
 def test_set_follows_tensors_that_change_type_or_layout(L):
     """A view of another type or stride that begins where the tensor did and has as
     many values: scaled as what it is, or refused, and nothing beside it is written."""
-    buf = made([200], TYPES[:1], 3)[0]
+    buf = made([200], TYPES[1:2], 3)[0].float()  # finite as bf16 too
     keep = buf.clone()
     g = buf[:100]
     s = L.LbqGradSet([g])
