@@ -23,8 +23,6 @@
 
 #include "lbq_device.h"
 
-#include <cmath>
-
 namespace lbq {
 
 namespace {
@@ -224,60 +222,10 @@ void launch(const DxSet& set, int64_t m, int64_t k, int ks, int per, uint16_t* d
                      dX, part, lora);
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// How an input gradient runs: by k_i8_dx with 16 tm tokens and ks ranges of `per`
-// slices, or (tm 0) by k_bwd_dx's bk x bm tiles.
-struct DxChoice {
-  int tm, ks, per;
-  int bk, bm;
-};
-constexpr double kMostPart = 256e6;  // bytes of sums of a split reduction
-
-// The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 300 input gradients (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights
-// not in cache): on these the choice is 2% off the best one on average.
-//  * k_i8_dx: a round is one workgroup a CU (their rings fill its LDS), and costs
-//    its slices at a rate that grows with the CUs at work; a split adds a second
-//    launch and the traffic of the sums.  (An estimate that went on linearly past
-//    one round chose 384 workgroups for 256 CUs: m = 40, n = 14336, k = 4096 34.8 us
-//    against 27.7 with four ranges.)
-//  * k_bwd_dx, per 64 rows: 0.713 a round of 128 x 128 tiles and 0.302, 1.20 a round
-//    of 256 x 128, 1.78 a round of 256 x 256.
-DxChoice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
-  static constexpr double kBase[3] = {2.27, 2.25, 2.43}, kRound[3] = {1.31, 1.45, 1.84}, kSlice[3] = {0.0675, 0.075, 0.0955},
-                          kShare[3] = {0.0192, 0.0215, 0.0366}, kRead[3] = {0.138e-6, 0.119e-6, 0.080e-6},
-                          kSums[3] = {2.77e-6, 2.38e-6, 2.10e-6};
-  int64_t slices = 0, n = 0;
-  for (int i = 0; i < count; ++i) slices += ceil_div(ns[i], 32), n += ns[i];
-  DxChoice best{};
-  double least = 1e30;
-  for (int t = 0; t < 3; ++t) {
-    const int tm = 1 << t;
-    for (int want : {1, 2, 3, 4, 6, 8}) {
-      const int per = (int)ceil_div(slices, want), ks = (int)ceil_div(slices, per);
-      if (ks > 1 && (!split || 4.0 * ks * m * k > kMostPart)) break;
-      const double r = (double)(k / 64 * ceil_div(m, 16 * tm)) * ks / 256, full = std::floor(r);
-      double us = kBase[t] + full * (kRound[t] + per * (kSlice[t] + kShare[t])) + kRead[t] * (double)n * k;
-      if (r > full) us += kRound[t] + per * (kSlice[t] + kShare[t] * (r - full));
-      if (ks > 1) us += 2.0 + kSums[t] * ks * m * k;
-      if (us < least) least = us, best = {tm, ks, per, 0, 0};
-    }
-  }
-  const double stages = std::ceil(n / 64.0);
-  const double t128 = 3.3 + stages * (0.713 * std::ceil(ceil_div(k, 128) * ceil_div(m, 128) / 256.0) + 0.302);
-  const double t256x128 = 4.2 + stages * 1.20 * std::ceil(ceil_div(k, 256) * ceil_div(m, 128) / 256.0);
-  const double t256 = 5.2 + stages * 1.78 * std::ceil(ceil_div(k, 256) * ceil_div(m, 256) / 256.0);
-  if (t128 < least) least = t128, best = {0, 1, 0, 128, 128};
-  if (t256x128 < least) least = t256x128, best = {0, 1, 0, 256, 128};
-  if (t256 < least) least = t256, best = {0, 1, 0, 256, 256};
-  return best;
-}
-
 }  // namespace
 
 size_t i8_dx_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
-  const DxChoice c = choose(ns, count, k, m, true);
+  const I8DxChoice c = i8_dx_choose(ns, count, k, m, true);
   return c.tm != 0 && c.ks > 1 ? (size_t)c.ks * (size_t)m * (size_t)k * sizeof(float) : 0;
 }
 
@@ -299,7 +247,7 @@ hipError_t launch_i8_dx(const WView* ws, const uint16_t* const* dys, int count, 
   const int64_t k = ws[0].k;
   const size_t need = i8_dx_workspace_bytes(ns, count, k, m);
   const bool split = need > 0 && part != nullptr && part_bytes >= need;
-  const DxChoice c = choose(ns, count, k, m, split || need == 0);
+  const I8DxChoice c = i8_dx_choose(ns, count, k, m, split || need == 0);
   if (c.tm == 0) return launch_bwd_dx_i8_tiles(ws, dys, count, c.bk, c.bm, m, dX, lora, s);
   if (c.ks > 1 && !split) return hipErrorInvalidValue;
   if (c.ks == 1) part = nullptr;

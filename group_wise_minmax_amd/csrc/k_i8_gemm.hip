@@ -24,7 +24,6 @@
 #include "lbq_device.h"
 
 #include <algorithm>
-#include <cmath>
 
 namespace lbq {
 
@@ -38,8 +37,6 @@ struct I8Stage {
   int8_t w[BN * 64];
   int8_t x[BM * 64];
 };
-
-constexpr int I8K = 64;
 
 // Channels of a token's partial sums: 16 bytes at a time for any n.
 __host__ __device__ constexpr int padded(int n) { return (n + 3) & ~3; }
@@ -299,20 +296,6 @@ __device__ __forceinline__ void i8_tile(const I8Set& set, const int8_t* __restri
   }
 }
 
-// Tiles of one launch: 256 x 256 outputs each, numbered over all the weights'
-// row tiles; the first `whole` of them by one workgroup each, the others cut
-// into `cut` pieces (2: 128 x 256, 4: 128 x 128).  With whole = 0 the pieces
-// themselves are numbered, nx x ny of them: workgroups that find their piece
-// past the end would leave the others to a part of the chip, since workgroups
-// go round the shader engines in turn (m = 128, n = 18965, k = 2624: 42.1 us
-// against 25.2).  With ks > 1 (only where nothing is whole) K is split into ks
-// ranges of `per` slices, gridDim.y of them, whose integer sums k_i8_reduce adds.
-struct I8Plan {
-  int nx, ny;
-  int whole, cut;
-  int ks, per;
-};
-
 template <bool LORA>
 __global__ __launch_bounds__(kGemmThreads, 1) void k_i8_gemm(I8Set set, I8Plan plan, const int8_t* __restrict__ Xq,
                                                             const float* __restrict__ xs, int m, int k, LoraEpi lora,
@@ -359,91 +342,6 @@ __global__ __launch_bounds__(256) void k_i8_reduce(I8Set set, const int* __restr
   i8_store(set, wi, mr < m ? xs[mr] : 0.f, v, mr, m, n0, lora);
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// How a product of count weights of ns channels runs: by k_i8_skinny with tiles
-// of 16 tn channels and 16 tm tokens, or (tn 0) by k_i8_gemm as `plan` says.
-struct I8Choice {
-  int tn, tm;
-  I8Plan plan;
-};
-
-constexpr int64_t kMostGridY = 65535;
-
-// Tiles of k_i8_skinny and what they cost (us): `base`, and a round of `room`
-// workgroups `start`, and for a 128-byte line of a wave `line` and, where all of the
-// room is taken, `share`; `read` for a byte of the weights.
-struct Skinny {
-  int tn, tm, room;
-  double base, start, line, share, read;
-};
-constexpr Skinny kSkinny[] = {{1, 1, 256, 2.38, 0.21, 0.401, 0.104, 0.110e-6}, {2, 1, 512, 2.33, 0.00, 0.615, 1.141, 0.122e-6},
-                              {4, 1, 256, 2.20, 0.00, 1.234, 0.344, 0.147e-6}, {2, 2, 256, 2.40, 0.00, 0.832, 0.356, 0.110e-6},
-                              {4, 2, 256, 1.51, 0.89, 1.288, 0.733, 0.131e-6}, {4, 4, 256, 1.28, 1.94, 1.599, 1.025, 0.109e-6}};
-
-// The cheapest by an estimate in microseconds, fitted to the times of all of
-// them on 1400 products (m 1 to 3000, n 256 to 28672, k 256 to 28672, weights not in
-// cache): on these the choice is 2.3% off the best one on average.
-//  * k_i8_skinny: rounds of workgroups, each at a rate for a 128-byte line of a wave
-//    that grows with the CUs at work.  (Its tokens are the grid's second dimension,
-//    which has 65535 workgroups.)
-//  * k_i8_gemm: the same with a rate for 64 of k: in 256 x 256 tiles whose last
-//    round is cut where it would leave half of the chip idle (128 x 256 pieces) or
-//    three quarters (128 x 128), or all in tiles or pieces of one size; 128 x 128
-//    pieces may split K, which costs a second launch and the traffic of the sums.
-I8Choice choose(const int64_t* ns, int count, int64_t k, int64_t m, bool split) {
-  // us of `groups` workgroups, `room` of them at a time: each costs `steps` steps
-  // of `step` and `share` where all of the room is taken
-  const auto rounds = [](double groups, int room, double start, double step, double share, double steps) {
-    const double r = groups / room, full = std::floor(r);
-    double us = full * (start + steps * (step + share));
-    if (r > full) us += start + steps * (step + share * (r - full));
-    return us;
-  };
-  I8Choice best{};
-  double least = 1e30;
-  int64_t n = 0, tiles = 0;
-  for (int i = 0; i < count; ++i) n += ns[i], tiles += ceil_div(ns[i], 256) * ceil_div(m, 256);
-  for (const Skinny& c : kSkinny) {
-    int64_t groups = 0;
-    if (ceil_div(m, 16 * c.tm) > kMostGridY) continue;
-    for (int j = 0; j < count; ++j) groups += ceil_div(ns[j], 16 * c.tn);
-    groups *= ceil_div(m, 16 * c.tm);
-    const double us = c.base + rounds((double)groups, c.room, c.start, c.line, c.share, (double)ceil_div(k, 1024)) +
-                      c.read * (double)n * k;
-    if (us < least) least = us, best.tn = c.tn, best.tm = c.tm;
-  }
-  const int slices = (int)(k / I8K);
-  const auto plan = [&](int64_t whole, int cut) {
-    I8Plan p{};
-    const int tn = whole > 0 ? 256 : 128;
-    for (int i = 0; i < count; ++i) p.nx += (int)ceil_div(ns[i], tn);
-    p.ny = (int)ceil_div(m, whole > 0 || cut == 2 ? 256 : 128);
-    p.whole = (int)whole, p.cut = cut, p.ks = 1, p.per = slices;
-    return p;
-  };
-  const auto consider = [&](I8Plan p) {
-    const int64_t pieces = p.whole > 0 ? (tiles - p.whole) * p.cut : (int64_t)p.nx * p.ny;
-    double us = 3.1 + (double)(n + m) * k * 0.070e-6 + rounds(p.whole, 256, 8.19, 0.357, 0.349, slices);
-    us += p.cut == 2 ? rounds((double)pieces, 256, 3.69, 0.309, 0.124, slices)
-                     : rounds((double)pieces * p.ks, 256, 1.96, 0.183, 0.078, p.per);
-    if (p.ks > 1) us += 3.4 + 0.44e-6 * 4 * p.ks * m * n;
-    if (us < least) least = us, best = {0, 0, p};
-  };
-  const int64_t rest = tiles % 256;
-  if (tiles > 256 && rest > 0 && rest <= 128) consider(plan(tiles - rest, rest <= 64 ? 4 : 2));
-  consider(plan(tiles, 2));
-  consider(plan(0, 2));
-  for (int ks = 1; ks <= 8; ++ks) {
-    if (ks > 1 && (!split || tiles > 64 || slices < 4 * ks)) break;
-    I8Plan p = plan(0, 4);
-    p.per = (int)ceil_div(slices, ks);
-    p.ks = (int)ceil_div(slices, p.per);
-    consider(p);
-  }
-  return best;
-}
-
 }  // namespace
 
 static size_t part_bytes(const I8Choice& c, const int64_t* ns, int count, int64_t m) {
@@ -454,7 +352,7 @@ static size_t part_bytes(const I8Choice& c, const int64_t* ns, int count, int64_
 }
 
 size_t i8_fwd_workspace_bytes(const int64_t* ns, int count, int64_t k, int64_t m) {
-  return part_bytes(choose(ns, count, k, m, true), ns, count, m);
+  return part_bytes(i8_choose(ns, count, k, m, true), ns, count, m);
 }
 
 I8Set i8_set(const WView* ws, uint16_t* const* ys, const int64_t* ldys, const int32_t* const* out_rows, int count) {
@@ -483,8 +381,8 @@ hipError_t launch_i8_fwd(const I8Set& weights, const int8_t* Xq, const float* xs
     ns[i] = set.n[i];
     most = std::max(most, set.n[i]);
   }
-  I8Choice c = choose(ns, set.count, k, m, true);
-  if (part_bytes(c, ns, set.count, m) > work_bytes) c = choose(ns, set.count, k, m, false);
+  I8Choice c = i8_choose(ns, set.count, k, m, true);
+  if (part_bytes(c, ns, set.count, m) > work_bytes) c = i8_choose(ns, set.count, k, m, false);
   if (c.tn != 0) return launch_i8_skinny(set, c.tn, c.tm, Xq, xs, m, k, lora, s);
   const I8Plan& plan = c.plan;
   for (int i = 0; i < set.count; ++i) set.tile_end[i] = end += (int)ceil_div(set.n[i], plan.whole > 0 ? 256 : 128);

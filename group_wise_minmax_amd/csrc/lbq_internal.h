@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "lbq.h"
+#include "lbq_i8_choice.h"
 
 namespace lbq {
 
@@ -214,9 +215,7 @@ hipError_t launch_i8_fwd(const I8Set& set, const int8_t* Xq, const float* xs, in
 // that split K over their waves; set.tile_end is not looked at.
 hipError_t launch_i8_skinny(const I8Set& set, int tn, int tm, const int8_t* Xq, const float* xs, int64_t m, int64_t k,
                             const LoraEpi& lora, hipStream_t s);
-// From bf16 tokens X [m][k] in one launch: m <= 4 and m * k <= kI8DecodeCodes.
-constexpr int kI8DecodeCodes = 16384;
-inline bool i8_decode_fits(int64_t m, int64_t k) { return m <= 4 && m * k <= kI8DecodeCodes; }
+// From bf16 tokens X [m][k] in one launch, where i8_decode_fits(m, k).
 hipError_t launch_i8_decode(const I8Set& set, const uint16_t* X, int64_t m, int64_t k, const LoraEpi& lora, const XaSums& t,
                             hipStream_t s);
 
