@@ -608,7 +608,8 @@ def lbq_linear_fwd_tokens(codes: torch.Tensor, scales: torch.Tensor, qw: Quantiz
 _GRAD_DTYPE = {torch.float32: LBQ_F32, torch.bfloat16: LBQ_BF16, torch.float16: LBQ_F16}
 _NORM_TYPE = {2.0: LBQ_NORM_2, float("inf"): LBQ_NORM_INF}
 # What a table entry says of a tensor.
-_ENTRY = (torch.Tensor.data_ptr, torch.Tensor.numel, operator.attrgetter("dtype"), torch.Tensor.is_contiguous)
+_PTR, _NUMEL, _CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+_DTYPE = operator.attrgetter("dtype")
 
 
 class LbqGradSet:
@@ -628,6 +629,7 @@ class LbqGradSet:
     def __init__(self, grads, outs=None):
         self._grads = list(grads)
         self._outs = self._grads if outs is None else list(outs)
+        self._tensors = self._grads if outs is None else self._grads + self._outs
         if not self._grads:
             raise ValueError("at least one gradient")
         if len(self._outs) != len(self._grads):
@@ -642,10 +644,8 @@ class LbqGradSet:
     def _look(self) -> None:
         """Fill the table from the tensors, unless all are as they were: another
         view's values may begin at the same address and be as many."""
-        seen = []
-        for ts in (self._grads,) if self._outs is self._grads else (self._grads, self._outs):
-            for what in _ENTRY:
-                seen += map(what, ts)
+        ts = self._tensors
+        seen = [*map(_PTR, ts), *map(_NUMEL, ts), *map(_DTYPE, ts), *map(_CONTIGUOUS, ts)]
         if seen == self._seen:
             return
         self._seen = None  # a refusal below leaves a table that is filled again

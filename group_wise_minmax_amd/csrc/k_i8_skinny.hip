@@ -4,7 +4,8 @@
 //
 // A workgroup computes 16 TN channels of 16 TM tokens (1, 2 or 4; more channels than
 // tokens where the tokens are few and would be fetched for every 16 channels again:
-// m = 12, n = 14336, k = 4096 17.6 us with 32 x 32, 16.4 with 64 x 16).  Its eight
+// m = 24, n = 14336, k = 4096 16.8 us with 64 x 32, 18.6 with 32 x 32; m = 39, n =
+// 5079, k = 5952 16.1 with 64 x 16, 17.3 with 32 x 32, 18.8 with 32 x 16).  Its eight
 // waves split K among them, a 128-byte line of every row by turns; each wave
 // loads its share straight to LDS into a ring of its own, so that it waits
 // for its own loads only and no barrier is needed, and multiplies it on
@@ -12,7 +13,8 @@
 // neighbouring lanes are in different rows, and the L1 serves a third as much:
 // m = 512, n = k = 4096 37.5 -> 29.3 us through LDS; with lines of 64 bytes the
 // two halves of a line are fetched by two waves: m = 3, n = 8192, k = 28672
-// 54.8 -> 49.1 us with whole lines.)  The waves' integer sums are added at the
+// 54.8 -> 49.1 us with whole lines.  That size itself goes to k_i8_gemm with K split
+// over workgroups, 48.8 us with the launch that adds the sums.)  The waves' integer sums are added at the
 // end: exact, so no split changes a bit, and no second launch is needed.  Bound
 // by memory where the weight is large (m = 3, n = 8192, k = 28672: 235 MB in 47 us,
 // 5.0 TB/s; m = 24, n = 14336, k = 4096: 60 MB in 14), by latency where it is

@@ -416,9 +416,6 @@ __device__ __forceinline__ float sum_splits16(const float* __restrict__ part, in
   return v;
 }
 
-// bf16 bits of an 8-bit product, which is a NaN for a token whose scale is one.
-__device__ __forceinline__ uint16_t i8_bf16(float f) { return (uint16_t)(cvt_pk_bf16(f, 0.f) & 0xFFFFu); }
-
 // 8-bit quantization of a row (k_i8_quant.hip has the rule).  Magnitudes are
 // compared as integers, the fp32 bits without the sign.
 // Largest magnitude of eight bf16 values.

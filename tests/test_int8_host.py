@@ -325,7 +325,7 @@ def host_set(L, grads, outs=None):
     """A set of CPU tensors, for its table alone (no call takes it)."""
     s = object.__new__(L.LbqGradSet)
     s._grads, s._outs, s.device = grads, grads if outs is None else outs, grads[0].device
-    s._table, s._seen = (L.Grad * len(grads))(), None
+    s._tensors, s._table, s._seen = grads + (outs or []), (L.Grad * len(grads))(), None
     s._look()
     return s
 
