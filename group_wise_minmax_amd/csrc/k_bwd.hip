@@ -412,7 +412,10 @@ __global__ __launch_bounds__(WGK* WGM * 64) void k_bwd_dx(BwdSet set, int m, uin
       // core and the vector unit at once, and two stages on their way instead of one
       // (a step takes about as long as a load).  m = 300, n = 4096, k = 14336: staged and
       // multiplied one after the other 86.5 us, interleaved 82.5, with two stages
-      // 77.6; 2048 tokens through q, k and v of 8B 123.7, 124.3, 120.0.  (Not for 128 x
+      // 77.6; 2048 tokens through q, k and v of 8B 123.7, 124.3, 120.0.  A stage takes 1.2
+      // us, some 2500 cycles: a SIMD has 1024 of MFMAs and near 1000 of the 250 other
+      // vector instructions of its two waves, which still run largely one after the
+      // other; 176 KiB through LDS would take 1400.  (Not for 128 x
       // 128 tiles of four waves: its registers leave no room for a second workgroup
       // on a CU, and two rounds become three: m = 300, n = 4096, k = 14336 97 and 136 us.)
       if (nt + 2 * BNR < N) {

@@ -7,12 +7,12 @@
 // kernel's arguments, so nothing is copied to the device and a captured launch
 // keeps it): one sums, one scales; with several tables one more launch adds up
 // all the partial sums.  Bound by memory: the gradients are read twice and
-// written once.  448 adapter gradients of rank 64 (671 MB): 400 us, the sums at
-// 5.1 TB/s and the scaling at 4.7 (read and written; a copy runs at 5.05).  The
-// scaling walks back from what the sums read last, which is still in the 256 MB
-// Infinity Cache (that table 43 us, the others 71).  Few small tensors are bound
-// by the two launches (4 of rank 16, 0.9 MB: 11.6 us a call, most of it on the
-// host).
+// written once.  448 adapter gradients of rank 64 (671 MB): 400 us, of them 130 the
+// sums, 5.2 TB/s, and 259 the scaling, 5.2 TB/s read and written (a copy runs at
+// 5.05).  The scaling walks back from what the sums read last, which is still in the
+// 256 MB Infinity Cache (that table 42 us, the others 72).  Few small tensors are
+// bound by the two launches (4 of rank 16, 0.9 MB: 12 us a call, 8.6 of them the
+// kernels and the rest the host).
 //
 // The squares are summed in fp64 (a square of any finite fp32 value is
 // finite there, and 10^9 of them lose nothing that fp32 could show).  Each

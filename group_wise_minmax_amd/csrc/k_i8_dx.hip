@@ -1,6 +1,10 @@
 // Input gradient through 8-bit weights for few outputs, dX = sum_i dY_i . deq(W_i)
 // with deq(W) = bf16(fl(q * s)) (m * k too small for k_bwd_dx's tiles to fill the
-// chip; that kernel, in k_bwd.hip, does the larger ones).
+// chip; that kernel, in k_bwd.hip, does the larger ones).  The weight is rounded to
+// bf16 for the MFMA, and is the weight that lbq_dequant writes, as for the other
+// formats: dX is off by 0.0023 of its norm, where fp32 weights would leave the 0.0017
+// of its own rounding; a second bf16 part of each weight would cost as many MFMAs
+// again.
 //
 // A workgroup computes 64 columns of dX (k) of 16 TM tokens; its eight waves
 // split the reduction over n among them, 32 rows of W at a time by turns, each

@@ -59,6 +59,8 @@ struct Chunk8<uint16_t> {
 // partial sums are loaded behind the row, which saves their own launch (m =
 // 2048, n = k = 4096, rank 16 63.8 -> 60.9 us; m = 64, rank 64 29.9 -> 23.9; the
 // whole product X A^T in this kernel, from the same registers, was slower: 65.8).
+// T is rounded to bf16, which the adapter term's MFMA takes: off by at most 2^-8 of T,
+// as Y is by its own rounding.
 // row0: the first row's place in t.
 template <typename T, int NT, int NC, bool KEEP>
 __global__ __launch_bounds__(NT) void k_i8_quant_rows(const T* __restrict__ X, int64_t ldx, int64_t k,

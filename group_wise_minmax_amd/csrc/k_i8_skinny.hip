@@ -13,16 +13,16 @@
 // neighbouring lanes are in different rows, and the L1 serves a third as much:
 // m = 512, n = k = 4096 37.5 -> 29.3 us through LDS; with lines of 64 bytes the
 // two halves of a line are fetched by two waves: m = 3, n = 8192, k = 28672
-// 54.8 -> 49.1 us with whole lines.  That size itself goes to k_i8_gemm with K split
-// over workgroups, 48.8 us with the launch that adds the sums.)  The waves' integer sums are added at the
-// end: exact, so no split changes a bit, and no second launch is needed.  Bound
-// by memory where the weight is large (m = 3, n = 8192, k = 28672: 235 MB in 47 us,
-// 5.0 TB/s; m = 24, n = 14336, k = 4096: 60 MB in 14), by latency where it is
-// small.
+// 54.8 -> 49.1 us with whole lines.  Given a workspace that size goes to k_i8_gemm
+// with K split over workgroups, 48.8 us with the launch that adds the sums against
+// 49.8 here.)  The waves' integer sums are added at the end: exact, so no split
+// changes a bit, and no second launch is needed.  Bound by memory where the weight
+// is large (m = 24, n = 14336, k = 4096: 60 MB in 13.4 us, 4.5 TB/s), by latency
+// where it is small (m = 130, n = 1001, k = 4160: 7.6 us).
 //
 // k_i8_decode is the same for up to 4 tokens that are short enough to be
 // quantized by every workgroup for itself while its first weights are on
-// their way: one launch from bf16 tokens to outputs (m = 1, n = k = 4096: 6.6 us).
+// their way: one launch from bf16 tokens to outputs (m = 1, n = k = 4096: 6.5 us).
 #pragma clang fp contract(off)
 
 #include "lbq_device.h"
@@ -61,8 +61,8 @@ __device__ __forceinline__ void barrier_lds() {
 }
 
 // U slots of a ring: with two for 32 x 32 a CU has room for two workgroups (m = 24, n
-// = 14336, k = 4096, 448 workgroups: four slots 19.9 us, two 18.9); 16 x 16 gains
-// nothing from fewer (16.2 and 16.5 us at m = 5).
+// = 14336, k = 4096 in these tiles, 448 workgroups: four slots 19.9 us, two 18.9);
+// 16 x 16 gains nothing from fewer (m = 5, the same weight: 16.2 and 16.5).
 template <int TN, int TM, int U>
 __global__ __launch_bounds__(kThreads) void k_i8_skinny(I8Set set, const int8_t* __restrict__ Xq,
                                                        const float* __restrict__ xs, int m, int k, LoraEpi lora) {

@@ -2,7 +2,8 @@
 // cannot allocate device memory (code under stream capture, tight serving
 // loops, harnesses that forbid hipMalloc).  The only scratch memory the
 // forward uses -- the fp32 split-K partial sums of the small-batch kernel
-// (2 <= m <= 64) and of GEMM launches that split K (m > 64) -- lives in a
+// (2 <= m <= 64) and of GEMM launches that split K (m > 64), or the codes and
+// scales of an INT8 weight's tokens and its integer partial sums -- lives in a
 // fixed array in the library's device image instead of a caller workspace;
 // inputs and outputs are still the caller's.
 //
@@ -12,8 +13,8 @@
 // with that device current, and that address is what the kernels receive.
 //
 // Every call on a device shares that device's array and leaves its contents
-// behind.  Nothing in it needs to start at zero: every partial sum is written
-// before it is read within the same call.  Calls that overlap on one device
+// behind.  Nothing in it needs to start at zero: everything is written before it
+// is read within the same call.  Calls that overlap on one device
 // (two streams, or two host threads) race on the array.
 #include <hip/hip_runtime.h>
 

@@ -13,7 +13,17 @@ constexpr int I8K = 64;  // codes in a slice of K
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Few short tokens are quantized by the product's own launch, k_i8_decode.
+// Few short tokens are quantized by the product's own launch, k_i8_decode: one
+// launch and no workspace where the others take a quantizer's launch first.  Called
+// one after another, that and one launch, in us (m x k through n):
+//   1 x 1024, 4096: 8.0, 5.5    1 x 4096, 4096: 9.2, 8.5    1 x 16384, 4096: 20.6, 19.3
+//   1 x 8192, 14336: 31.2, 26.8  1 x 16384, 14336: 58.2, 50.0  4 x 4096, 4096: 10.3, 10.2
+// and, where the tokens are short and the channels many, so that every workgroup's
+// quantizing counts, it loses:
+//   1 x 1024, 14336: 8.6, 10.0  4 x 1024, 14336: 8.7, 10.5  4 x 4096, 14336: 18.8, 21.2
+// The limit is what leaves two workgroups on a CU (48 KiB of rings and the codes):
+// with twice as many codes 1 x 4096 through 14336 takes 26.8 instead of 18.2, and 1 x
+// 28672 through 4096 30.2 where two launches take 31.2.
 constexpr int kI8DecodeCodes = 16384;
 inline bool i8_decode_fits(int64_t m, int64_t k) { return m <= 4 && m * k <= kI8DecodeCodes; }
 
