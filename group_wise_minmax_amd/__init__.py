@@ -185,8 +185,9 @@ class QuantizedWeight:
         nbytes = lib.lbq_serialized_bytes(ctypes.byref(self.desc))
         buf = ctypes.create_string_buffer(nbytes)
         q = self.qtensor()
-        check(lib.lbq_serialize(ctypes.byref(self.desc), ctypes.byref(q), buf, nbytes, _stream(self.device)),
-              "lbq_serialize")
+        with _on(self.device):
+            check(lib.lbq_serialize(ctypes.byref(self.desc), ctypes.byref(q), buf, nbytes, _stream(self.device)),
+                  "lbq_serialize")
         return buf.raw
 
     @staticmethod
@@ -196,7 +197,8 @@ class QuantizedWeight:
         check(lib.lbq_blob_desc(blob, len(blob), ctypes.byref(desc)), "lbq_blob_desc")
         qw = QuantizedWeight.empty(desc, device)
         q = qw.qtensor()
-        check(lib.lbq_deserialize(blob, len(blob), ctypes.byref(q), _stream(qw.device)), "lbq_deserialize")
+        with _on(qw.device):
+            check(lib.lbq_deserialize(blob, len(blob), ctypes.byref(q), _stream(qw.device)), "lbq_deserialize")
         return qw
 
     def storage_view(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:

@@ -386,3 +386,39 @@ def test_set_fills_its_table_again_after_a_refusal(L):
     a.data, b.data = at, bt
     s._look()
     assert entries(s) == want
+
+
+def test_serialization_runs_on_the_weights_device(L, monkeypatch):
+    """The copies go to a stream of the weight's device: that device is current
+    around them (a default stream is the current device's)."""
+    import contextlib
+    import types
+
+    import torch
+    qw = L.QuantizedWeight.empty(L.make_desc("int8", 3, 64), "cpu")
+    blob = bytes(96 + 192 + 16)
+    inside, calls = [], []
+
+    @contextlib.contextmanager
+    def on(device):
+        inside.append(device)
+        yield
+        inside.pop()
+
+    def copies(*args):
+        calls.append(list(inside))
+        return 0
+
+    def desc_of(_blob, _size, d):
+        d._obj.__init__(*[getattr(qw.desc, f) for f, _ in L.Desc._fields_])
+        return 0
+
+    fake = types.SimpleNamespace(lbq_serialize=copies, lbq_deserialize=copies, lbq_blob_desc=desc_of,
+                                 lbq_serialized_bytes=lambda d: len(blob), lbq_layout=L.lib.lbq_layout)
+    monkeypatch.setattr(L, "lib", fake)
+    monkeypatch.setattr(L, "_on", on)
+    monkeypatch.setattr(L, "_stream", lambda device: None)
+    assert len(qw.to_bytes()) == len(blob)
+    back = L.QuantizedWeight.from_bytes(blob, "cpu")
+    assert (back.n, back.k) == (3, 64)
+    assert calls == [[torch.device("cpu")]] * 2
