@@ -264,7 +264,7 @@ size_t align16(size_t b) { return (b + 15) / 16 * 16; }
 // Workspace of the forward of INT8 weights that share X (16-byte aligned
 // pieces): the tokens' codes [m][k] and scales [m], then what the product
 // takes; none where one launch quantizes and multiplies.
-// (0 as well for sizes that the calls refuse)
+// (0 as well for rows of X that the calls refuse)
 bool i8_rows_fit(int64_t m, int64_t k) {
   return m >= 1 && m < (int64_t(1) << 31) && (uint64_t)(m + 256) * (uint64_t)k * 2 < (uint64_t(1) << 32);
 }

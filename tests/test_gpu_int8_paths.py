@@ -126,6 +126,29 @@ def test_adapted_products(L, case, r):
     assert bool((adapter.abs() > 4 * tol).any())  # a missing adapter term would show
 
 
+@pytest.mark.parametrize("case", [c for c in P.PRODUCTS if len(c[3]) == 1][::2] + [("decode", 3, 1024, (1001,))], ids=P.named)
+def test_adapted_products_scattered(L, case):
+    """The same bits into scattered channels, and into rows of a wider output."""
+    _, m, k, (n,) = case
+    (qw, _, _), = weights(L, (n,), k, m + k)
+    x = tokens(m, k, m)
+    g = generator(2)
+    A = (torch.randn((24, k), generator=g, device=DEV) * 0.05).to(torch.bfloat16)
+    B = torch.randn((n, 24), generator=g, device=DEV).to(torch.bfloat16)
+    want = L.lbq_lora_fwd(x, qw, A, B, 0.5)
+    out = torch.full((m, n + 9), -7.0, dtype=torch.bfloat16, device=DEV)
+    L.lbq_lora_fwd(x, qw, A, B, 0.5, out=out[:, 3:3 + n])
+    equal(out[:, 3:3 + n].contiguous(), want)
+    out[:, 3:3 + n] = -7.0
+    assert (out == -7.0).all()
+    at = torch.randperm(n + 9, generator=g, device=DEV)[:n]
+    qw.out_rows = at.to(torch.int32)
+    L.lbq_lora_fwd(x, qw, A, B, 0.5, out=out)
+    equal(out[:, at], want)
+    out[:, at] = -7.0
+    assert (out == -7.0).all()
+
+
 def gradient(dys, made):
     """dX in 64 bits, and what its fp32 sums and its rounding may be off by."""
     whats = [(q.float() * s).to(torch.bfloat16).double() for _, q, s in made]
