@@ -18,9 +18,9 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one after another, that and one launch, in us (m x k through n):
 //   1 x 1024, 4096: 8.0, 5.5    1 x 4096, 4096: 9.2, 8.5    1 x 16384, 4096: 20.6, 19.3
 //   1 x 8192, 14336: 31.2, 26.8  1 x 16384, 14336: 58.2, 50.0  4 x 4096, 4096: 10.3, 10.2
-// and, where the tokens are short and the channels many, so that every workgroup's
-// quantizing counts, it loses:
-//   1 x 1024, 14336: 8.6, 10.0  4 x 1024, 14336: 8.7, 10.5  4 x 4096, 14336: 18.8, 21.2
+// and, where there are many workgroups or several longer tokens, each workgroup's
+// quantizing costs more than the launch it saves:
+//   1 x 1024, 14336: 8.6, 10.0  4 x 4096, 14336: 18.8, 21.2    2 x 8192, 4096: 12.4, 13.5
 // The limit is what leaves two workgroups on a CU (48 KiB of rings and the codes):
 // with twice as many codes 1 x 4096 through 14336 takes 26.8 instead of 18.2, and 1 x
 // 28672 through 4096 30.2 where two launches take 31.2.
