@@ -235,3 +235,53 @@ def test_adapted_gradients(L, case, r):
     tol = torch.mm(dYt.abs(), t_err) + 2 * (m + 4) * E32 * torch.mm(dYt.abs(), T.abs()) + 1e-38
     tol = tol * (1 + HALF)
     assert bool(((dB.double() - torch.mm(dYt, T)).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("m", [1, 40, 300, 1300])
+def test_captured_training_calls(L, m):
+    """A set's forward and input gradient and an adapted layer's backward, captured
+    together and replayed with new inputs beside eager calls on the same weights;
+    then the same calls on two streams at once."""
+    k, ns, r = 1088, (512, 64, 192), 24
+    made = weights(L, ns, k, 7)
+    qws = [qw for qw, _, _ in made]
+    g = generator(m)
+
+    def draw(shape, scale):
+        return (torch.randn(shape, generator=g, device=DEV) * scale).to(torch.bfloat16)
+
+    x, dys = draw((m, k), 1.0), [draw((m, n), 0.01) for n in ns]
+    A, B = draw((r, k), 0.05), draw((ns[0], r), 0.05)
+
+    def step():
+        ys = L.lbq_linear_fwd_grouped(x, qws)
+        return [*ys, L.lbq_linear_bwd_dx_grouped(dys, qws), *L.lbq_lora_bwd(x, dys[0], qws[0], A, B, 0.5)]
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(4):
+        x.copy_(draw((m, k), 1.0))
+        for d in dys:
+            d.copy_(draw(d.shape, 0.01))
+        for o in outs:
+            o.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    want = step()
+    torch.cuda.synchronize()
+    streams, runs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for turn in range(6):
+        with torch.cuda.stream(streams[turn % 2]):
+            runs.append(step())
+    torch.cuda.synchronize()
+    for run in runs:
+        assert all(torch.equal(a, b) for a, b in zip(run, want))
