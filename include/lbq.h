@@ -417,8 +417,8 @@ typedef struct {
   int32_t reserved; /* 0 */
 } lbq_grad;
 
-/* Workspace bytes the two calls below take (0 as well for a list that they
- * refuse). */
+/* Workspace bytes the two calls below take (0 as well where they refuse a
+ * type, a size or a gradient's address). */
 size_t lbq_grad_workspace_bytes(int32_t count, const lbq_grad* grads);
 
 /* Norm over all the values of `count` tensors (count >= 1; a tensor listed
